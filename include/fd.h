@@ -19,9 +19,9 @@
  * Conventions shared by every entry point:
  *  - Tensor pointers are DEVICE pointers owned by the caller. The library
  *    keeps no pointer and allocates nothing; the workspace is caller-supplied.
- *  - Element types: q and out are bf16; K and V are bf16 or fp8 E4M3 codes
- *    (fd_problem.kv_dtype); lse, the workspace and scale are fp32; seqlens
- *    and block_table are int32.
+ *  - Element types: q and out are bf16; K and V are bf16, fp8 E4M3 codes or
+ *    4-bit codes (fd_problem.kv_dtype); lse, the workspace and scale are fp32;
+ *    seqlens and block_table are int32.
  *  - Errors are return codes. No entry point aborts, throws or prints.
  *    Argument checks run on the host before anything is launched; an invalid
  *    call launches nothing.
@@ -78,7 +78,10 @@ typedef enum fd_kv_layout {
 /* Element type of the K/V cache. */
 typedef enum fd_kv_dtype {
   FD_KV_BF16 = 0,     /* bf16 */
-  FD_KV_FP8_E4M3 = 1  /* OCP fp8 e4m3 (bias 7, max 448, no inf); value = scale * code */
+  FD_KV_FP8_E4M3 = 1, /* OCP fp8 e4m3 (bias 7, max 448, no inf); value = scale * code */
+  FD_KV_INT4 = 2      /* 4-bit codes with a scale and a bias per half row; for the entry points
+                       * named fd_*_int4 (see fd_append_int4 for the format) and
+                       * fd_plan_problem */
 } fd_kv_dtype;
 
 /* Tensor-core path of an fp8 cache.
@@ -111,7 +114,7 @@ typedef enum fd_fp8_mma {
  *   kv_dtype    an fd_kv_dtype value (FD_KV_BF16 when zero-initialised)
  *   k_scale, v_scale
  *               fp8 caches: the real K and V are k_scale * code and
- *               v_scale * code (finite, > 0). Ignored for bf16 caches.
+ *               v_scale * code (finite, > 0). Ignored for other caches.
  *               An fp8 cache needs D = 128; on the default path the
  *               contraction runs on f16 tensor cores, so q must be finite
  *               in f16 (|q| < 65504).
@@ -166,8 +169,9 @@ FD_API int fd_plan_seqlens(int num_sms, int B, int Hq, int Hkv, int D, int max_l
 
 /* The planner for a whole problem description: the same cost model, with
  * the cache's element type (an fp8 CTA moves half the bytes of a bf16 one
- * at the same token rate, so fp8 caches want more CTAs in flight) and, when
- * given, the lengths. fd_plan and fd_plan_seqlens plan for bf16 caches.
+ * at the same token rate, so fp8 caches want more CTAs in flight; a 4-bit one
+ * about a quarter) and, when given, the lengths. fd_plan and fd_plan_seqlens
+ * plan for bf16 caches.
  *   num_sms   SM count to plan for; <= 0 means the current device's
  *   p         HOST pointer to the problem as passed to fd_decode (pointers
  *             and scales are not read)
@@ -348,6 +352,132 @@ FD_API fd_status fd_decode_sparse(const fd_problem* p, const void* q, const void
                                   float delta, int num_splits, void* out, float* lse,
                                   uint8_t* kept, void* workspace, size_t workspace_bytes,
                                   fd_stream_t stream);
+
+/* ---- a KV cache held in 4 bits ----------------------------------------------
+ *
+ * A row of the cache is one token of one KV head: D entries (64 or 128) in two
+ * groups of D / 2. An entry of a group is held as a code c in 0..15, the group
+ * has a bf16 scale s and a bf16 bias b, and the entry stands for s (c - 8) + b.
+ *   k4, v4   uint8, D / 2 bytes per row, entry 2j in the low nibble of byte j,
+ *            in the orders of fd_decode's caches with D / 2 for D:
+ *            [B, Hkv, max_len, D/2], [num_blocks, Hkv, block_size, D/2],
+ *            [B, max_len, Hkv, D/2] or [num_blocks, block_size, Hkv, D/2]
+ *   params   bf16, one record of 8 per row, the same orders with 8 for D / 2:
+ *            ks0 kb0 ks1 kb1 vs0 vb0 vs1 vb1 (scale and bias of K's groups,
+ *            then of V's)
+ * All three are 16-byte aligned and row-major. A row takes D + 16 bytes for K
+ * and V together: 4.5 bits an entry at D = 128, 5 at D = 64 (bf16: 16).
+ * fd_problem describes the cache as for fd_decode, with kv_dtype = FD_KV_INT4;
+ * k_scale, v_scale and fp8_mma are ignored. The entry points below return
+ * FD_ERR_INVALID_ARGUMENT for another kv_dtype; fd_decode and the other entry
+ * points return it for FD_KV_INT4. */
+
+/* Quantises new K and V rows and writes them into a 4-bit cache. Per group of
+ * a row, with mn and mx its smallest and largest entry:
+ *   s = bf16((mx - mn) / 15)     b = bf16(mn + 8 s)
+ *   c = clamp(rint((x - b) / s), -8, 7) + 8
+ * in fp32, rounding to nearest, ties to even ((mx - mn) / 15 is rounded to fp32
+ * before bf16; mn + 8 s is rounded once to fp32, then to bf16). A group whose
+ * entries are all equal gets s = 0, c = 8. A group that holds a NaN or an
+ * infinity gets s = b = NaN, so that attention over it gives NaN, as it does
+ * over a bf16 cache.
+ *   p         the cache (max_blocks_per_seq and max_len are checked, not used,
+ *             when it is paged; Hq only as Hq % Hkv)
+ *   n_tokens  rows of k_new and v_new, >= 0; 0 launches nothing
+ *   k_new, v_new
+ *             bf16, 16-byte aligned: token i, head h starts at element
+ *             i * k_stride + h * D (v_stride for V), so that slices of a fused
+ *             projection's output are read where they lie. Strides count
+ *             elements, are multiples of 8 and at least Hkv * D.
+ *   slots     [n_tokens] int64, 8-byte aligned: the place of each token,
+ *             page * block_size + row in a paged cache and b * max_len + t in
+ *             a contiguous one. A token whose slot is negative or outside the
+ *             cache is skipped. A slot may appear once; of two tokens with the
+ *             same slot either one's codes or records may be found there.
+ * Rows of other slots are left as they were. */
+FD_API fd_status fd_append_int4(const fd_problem* p, int n_tokens, const void* k_new,
+                                int64_t k_stride, const void* v_new, int64_t v_stride,
+                                const int64_t* slots, void* k4, void* v4, void* params,
+                                fd_stream_t stream);
+
+/* The rows of a 4-bit cache as a contiguous bf16 cache: s (c - 8) + b, rounded
+ * to fp32 and then to bf16. The result is a cache for fd_decode and the entry
+ * points beside it, and what the attention of a prompt reads when it is to see
+ * the same K and V as the later steps.
+ *   k4, v4, params, seqlens, block_table   as for fd_decode_int4
+ *   k_out, v_out   bf16, 16-byte aligned: [B, Hkv, max_len, D]
+ *                  (FD_LAYOUT_HND) or [B, max_len, Hkv, D] (FD_LAYOUT_NHD),
+ *                  with p's max_len for a paged cache too. Rows at or past a
+ *                  sequence's length are left as they were. A page id outside
+ *                  [0, num_blocks) gives zeros. */
+FD_API fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void* v4,
+                                const void* params, const int32_t* seqlens,
+                                const int32_t* block_table, void* k_out, void* v_out,
+                                fd_stream_t stream);
+
+/* Decode attention over a 4-bit cache: fd_decode over the values that the
+ * codes stand for. D is 64 or 128; G, layouts, pages, lengths, the split cut,
+ * the workspace and the results are those of fd_decode (fd_plan_problem gives
+ * the split count). Scores and sums are taken in fp32; a softmax weight enters
+ * the product with V's codes as weight * scale, rounded to f16 (11 significant
+ * bits) relative to the largest scale seen. Rows at or past a sequence's
+ * length may hold anything. A page id outside [0, num_blocks) reads zeros. */
+FD_API fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4,
+                                const void* v4, const void* params, const int32_t* seqlens,
+                                const int32_t* block_table, float scale, int num_splits,
+                                void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                fd_stream_t stream);
+
+/* ---- pages of a paged cache, kept on the device -------------------------------
+ *
+ * The pool's free pages are a stack: free_pages[0 .. free_count - 1], with
+ * free_pages of num_pages entries. Both calls are functions of device memory
+ * alone, with no wait on the host, so that a decode loop can be captured. The
+ * new lengths and the new count may be written over the old ones
+ * (seqlens_out == seqlens, free_count_out == free_count) or elsewhere; no other
+ * output may share memory with an input or with another output.
+ * B is in [1, 65535], block_size a power of two in [8, 256]
+ * (FD_ERR_UNSUPPORTED otherwise). Lengths are clamped to [0,
+ * max_blocks_per_seq * block_size], free_count to [0, num_pages]. */
+
+/* Pages and slots for the new tokens of a batch. Request b holds seqlens[b]
+ * tokens and gets new_lens[b] more (negative: 0): in the order of the requests
+ * each takes from the top of the stack the pages that its new tokens need
+ * beyond those it has, and they are written into its row of block_table (other
+ * entries are left as they were). The new tokens of all requests are listed
+ * one request after another:
+ *   cu_new     [B + 1] int32: request b's are cu_new[b] .. cu_new[b + 1] - 1;
+ *              the list ends at max_tokens, and what is beyond it is not
+ *              listed and not counted
+ *   slots      [max_tokens] int64, 8-byte aligned: page * block_size + row of
+ *              each new token, as fd_append_int4 takes them; -1 where the
+ *              request's table row or the pool is exhausted, and behind the
+ *              last token
+ *   positions  [max_tokens] int32 or NULL: the token's index in its sequence;
+ *              0 behind the last token
+ *   seqlens_out     [B] int32: tokens that have a place. Less than seqlens[b] +
+ *                   new_lens[b] when the request could not be served in full.
+ *   free_count_out  [1] int32: pages still free
+ * max_tokens is >= 0 (slots may be NULL when it is 0). */
+FD_API fd_status fd_alloc_pages(int B, int block_size, int max_blocks_per_seq, int max_tokens,
+                                int num_pages, const int32_t* seqlens, const int32_t* new_lens,
+                                const int32_t* free_pages, const int32_t* free_count,
+                                int32_t* block_table, int32_t* seqlens_out, int32_t* cu_new,
+                                int64_t* slots, int32_t* positions, int32_t* free_count_out,
+                                fd_stream_t stream);
+
+/* Gives the pages of finished requests back. Request b is finished when
+ * done[b] is not 0: the ceil(seqlens[b] / block_size) pages of its table row go
+ * on top of the stack, in the order of the requests, and its length becomes 0.
+ * Pages that do not fit num_pages are dropped.
+ *   done            [B] uint8
+ *   seqlens_out     [B] int32: 0 for a finished request, its length otherwise
+ *   free_count_out  [1] int32 */
+FD_API fd_status fd_release_pages(int B, int block_size, int max_blocks_per_seq, int num_pages,
+                                  const int32_t* seqlens, const uint8_t* done,
+                                  const int32_t* block_table, int32_t* free_pages,
+                                  const int32_t* free_count, int32_t* seqlens_out,
+                                  int32_t* free_count_out, fd_stream_t stream);
 
 /* Largest workspace, in bytes, that fd_decode_static_workspace can use. */
 #define FD_STATIC_WORKSPACE_BYTES (8u << 20)

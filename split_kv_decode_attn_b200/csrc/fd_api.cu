@@ -13,7 +13,9 @@
 #include <mutex>
 
 #include "../../include/fd.h"
+#include "fd_int4.cuh"
 #include "fd_kernels.cuh"
+#include "fd_pages.cuh"
 
 namespace {
 
@@ -717,15 +719,22 @@ fd_status decode_impl(const fd_problem* p, const void* q, const void* k_cache,
   return r;
 }
 
-// The planner over every input it uses.  elem_bytes: bytes of one cache
-// element; seqlens: host lengths or null (every sequence holds max_len).
-int plan_impl(int num_sms, int B, int Hkv, int D, int max_len, int block_size, int elem_bytes,
+// K + V bytes of one token of one KV head.
+double kv_token_bytes(int kv_dtype, int D) {
+  if (kv_dtype == FD_KV_INT4) return D + 16.0;   // D / 2 bytes of codes each, and the record
+  return 2.0 * D * (kv_dtype == FD_KV_FP8_E4M3 ? 1 : 2);
+}
+
+// The planner over every input it uses.  seqlens: host lengths or null (every
+// sequence holds max_len).
+int plan_impl(int num_sms, int B, int Hkv, int D, int max_len, int block_size, int kv_dtype,
               const int32_t* seqlens) {
   // Two CTAs per slot from the batch alone: no split (this also bounds the
   // planning cost for large batches).
   if (static_cast<long long>(B) * Hkv >= 2LL * num_sms * fd::kCtasPerSm) return 1;
-  const PlanShape ps{num_sms, B, Hkv, 2.0 * D * elem_bytes,
-                     block_size > 0 && block_size < fd::kTile, D == 128, elem_bytes == 1};
+  const PlanShape ps{num_sms, B, Hkv, kv_token_bytes(kv_dtype, D),
+                     block_size > 0 && block_size < fd::kTile, D == 128,
+                     kv_dtype == FD_KV_FP8_E4M3};
   const long long units = static_cast<long long>(B) * Hkv;
   const int slots = num_sms * fd::kCtasPerSm;
   if (seqlens)
@@ -766,7 +775,7 @@ int fd_plan_sm(int num_sms, int B, int Hq, int Hkv, int D, int max_len, int bloc
   if (num_sms < 1) return FD_ERR_INVALID_ARGUMENT;
   const fd_status st = check_shape(B, Hq, Hkv, D, max_len, block_size);
   if (st != FD_OK) return st;
-  return plan_impl(num_sms, B, Hkv, D, max_len, block_size, 2, nullptr);
+  return plan_impl(num_sms, B, Hkv, D, max_len, block_size, FD_KV_BF16, nullptr);
 }
 
 int fd_plan_seqlens(int num_sms, int B, int Hq, int Hkv, int D, int max_len, int block_size,
@@ -778,21 +787,21 @@ int fd_plan_seqlens(int num_sms, int B, int Hq, int Hkv, int D, int max_len, int
     int dev = 0;
     if (current_device(&dev) != FD_OK || device_sms(dev, &num_sms) != FD_OK) return FD_ERR_CUDA;
   }
-  return plan_impl(num_sms, B, Hkv, D, max_len, block_size, 2, seqlens);
+  return plan_impl(num_sms, B, Hkv, D, max_len, block_size, FD_KV_BF16, seqlens);
 }
 
 int fd_plan_problem(int num_sms, const fd_problem* p, const int32_t* seqlens) {
   if (!p) return FD_ERR_INVALID_ARGUMENT;
   const fd_status st = check_shape(p->B, p->Hq, p->Hkv, p->D, p->max_len, p->block_size);
   if (st != FD_OK) return st;
-  if (p->kv_dtype != FD_KV_BF16 && p->kv_dtype != FD_KV_FP8_E4M3) return FD_ERR_INVALID_ARGUMENT;
+  if (p->kv_dtype != FD_KV_BF16 && p->kv_dtype != FD_KV_FP8_E4M3 && p->kv_dtype != FD_KV_INT4)
+    return FD_ERR_INVALID_ARGUMENT;
   if (p->kv_dtype == FD_KV_FP8_E4M3 && p->D != 128) return FD_ERR_UNSUPPORTED;
   if (num_sms < 1) {
     int dev = 0;
     if (current_device(&dev) != FD_OK || device_sms(dev, &num_sms) != FD_OK) return FD_ERR_CUDA;
   }
-  return plan_impl(num_sms, p->B, p->Hkv, p->D, p->max_len, p->block_size,
-                   p->kv_dtype == FD_KV_FP8_E4M3 ? 1 : 2, seqlens);
+  return plan_impl(num_sms, p->B, p->Hkv, p->D, p->max_len, p->block_size, p->kv_dtype, seqlens);
 }
 
 int fd_plan(int B, int Hq, int Hkv, int D, int max_len, int block_size) {
@@ -989,3 +998,5 @@ fd_status fd_check_device_error(fd_stream_t stream) {
 }
 
 }  // extern "C"
+
+#include "fd_int4_api.cuh"

@@ -1,0 +1,283 @@
+// fd_int4_api.cuh — host side of the 4-bit cache and of the page bookkeeping:
+// argument checks and launches.  Part of fd_api.cu, whose helpers it uses; see
+// include/fd.h for the contract of every entry point.
+#pragma once
+
+namespace {
+
+// The cache that p describes, checked: FD_KV_INT4, paged exactly when
+// block_table is given (paged caches that need no table pass any_table).
+fd_status int4_cache(const fd_problem* p, const void* k4, const void* v4, const void* params,
+                     fd::Int4Cache* c) {
+  if (!p || !k4 || !v4 || !params) return FD_ERR_INVALID_ARGUMENT;
+  const fd_status st = check_shape(p->B, p->Hq, p->Hkv, p->D, p->max_len, p->block_size);
+  if (st != FD_OK) return st;
+  if (p->kv_layout != FD_LAYOUT_HND && p->kv_layout != FD_LAYOUT_NHD) return FD_ERR_INVALID_ARGUMENT;
+  if (p->kv_dtype != FD_KV_INT4) return FD_ERR_INVALID_ARGUMENT;
+  if (p->block_size != 0) {
+    if (p->num_blocks < 1 || p->max_blocks_per_seq < 1) return FD_ERR_INVALID_ARGUMENT;
+    if (static_cast<long long>(p->max_blocks_per_seq) * p->block_size < p->max_len)
+      return FD_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(k4, 16) || !aligned(v4, 16) || !aligned(params, 16)) return FD_ERR_INVALID_ARGUMENT;
+  c->k4 = static_cast<uint8_t*>(const_cast<void*>(k4));
+  c->v4 = static_cast<uint8_t*>(const_cast<void*>(v4));
+  c->params = static_cast<uint8_t*>(const_cast<void*>(params));
+  c->planes = p->block_size ? p->num_blocks : p->B;
+  c->rows = p->block_size ? p->block_size : p->max_len;
+  c->Hkv = p->Hkv;
+  c->nhd = p->kv_layout == FD_LAYOUT_NHD;
+  return FD_OK;
+}
+
+fd_status this_device(int* dev) {
+  if (current_device(dev) != FD_OK) return FD_ERR_CUDA;
+  return device_is_sm100(*dev);
+}
+
+// Launches that may start while the previous kernel of the stream ends (every
+// kernel waits for it before its first read).
+template <class Kernel, class... Args>
+fd_status launch_chained(Kernel kernel, dim3 grid, int threads, size_t smem, fd_stream_t stream,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+template <int D>
+fd_status launch_split_int4(const fd::Int4DecodeArgs& a, dim3 grid, fd_stream_t s) {
+  const int threads = fd::kInt4Warps * 32;
+  switch (a.a.G) {
+    case 1: return launch_chained(fd::fd_split_int4_kernel<D, 1>, grid, threads, 0, s, a);
+    case 2: return launch_chained(fd::fd_split_int4_kernel<D, 2>, grid, threads, 0, s, a);
+    case 4: return launch_chained(fd::fd_split_int4_kernel<D, 4>, grid, threads, 0, s, a);
+    case 8: return launch_chained(fd::fd_split_int4_kernel<D, 8>, grid, threads, 0, s, a);
+    default: return launch_chained(fd::fd_split_int4_kernel<D, 16>, grid, threads, 0, s, a);
+  }
+}
+
+// Do two arrays of int32 share memory?
+bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b + 4 * ny && b < a + 4 * nx;
+}
+
+fd_status check_pages(int B, int block_size, int max_blocks_per_seq, int num_pages) {
+  if (B < 1 || B > 65535 || max_blocks_per_seq < 1 || num_pages < 1 || block_size < 1)
+    return FD_ERR_INVALID_ARGUMENT;
+  if (!is_pow2(block_size) || block_size < 8 || block_size > 256) return FD_ERR_UNSUPPORTED;
+  return FD_OK;
+}
+
+// One launch expands and writes the state.  When the new state lies over the
+// old one and several CTAs read the old, a second launch writes the state.
+template <class Kernel>
+fd_status launch_pages(Kernel kernel, fd::PageArgs a, long long items, fd_stream_t s) {
+  int dev = 0;
+  const fd_status st = this_device(&dev);
+  if (st != FD_OK) return st;
+  int sms = 0;
+  if (device_sms(dev, &sms) != FD_OK) return FD_ERR_CUDA;
+  const long long per = std::max<long long>(fd::kPageThreads, (items + 2LL * sms - 1) / (2LL * sms));
+  const int grid = static_cast<int>(std::max<long long>(1, (items + per - 1) / per));
+  const bool in_place = overlap(a.seqlens, a.B, a.seqlens_out, a.B) ||
+                        overlap(a.free_count, 1, a.free_count_out, 1);
+  a.items_per_cta = static_cast<int>(per);
+  a.write_items = true;
+  a.write_state = grid == 1 || !in_place;
+  fd_status r = launch_chained(kernel, dim3(static_cast<unsigned>(grid)), fd::kPageThreads, 0, s, a);
+  if (r == FD_OK && !a.write_state) {
+    a.write_items = false;
+    a.write_state = true;
+    r = launch_chained(kernel, dim3(1), fd::kPageThreads, 0, s, a);
+  }
+  return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+fd_status fd_append_int4(const fd_problem* p, int n_tokens, const void* k_new, int64_t k_stride,
+                         const void* v_new, int64_t v_stride, const int64_t* slots, void* k4,
+                         void* v4, void* params, fd_stream_t stream) {
+  fd::AppendArgs a{};
+  const fd_status st = int4_cache(p, k4, v4, params, &a.c);
+  if (st != FD_OK) return st;
+  if (n_tokens < 0 || !k_new || !v_new || !slots) return FD_ERR_INVALID_ARGUMENT;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8)) return FD_ERR_INVALID_ARGUMENT;
+  // Tokens start 16 bytes aligned and do not overlap.
+  const int64_t row = static_cast<int64_t>(p->Hkv) * p->D;
+  if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < row || v_stride < row)
+    return FD_ERR_INVALID_ARGUMENT;
+  if (n_tokens == 0 || a.c.rows == 0) return FD_OK;
+  int dev = 0;
+  const fd_status arch = this_device(&dev);
+  if (arch != FD_OK) return arch;
+  a.k = static_cast<const __nv_bfloat16*>(k_new);
+  a.v = static_cast<const __nv_bfloat16*>(v_new);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slots = slots;
+  a.n_tokens = n_tokens;
+  const long long rows = static_cast<long long>(n_tokens) * 2 * p->Hkv;
+  const long long per = 256 / (p->D / 8);
+  const long long grid = (rows + per - 1) / per;
+  if (grid > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
+  const dim3 g(static_cast<unsigned>(grid));
+  return p->D == 128 ? launch_chained(fd::fd_append_int4_kernel<128>, g, 256, 0, stream, a)
+                     : launch_chained(fd::fd_append_int4_kernel<64>, g, 256, 0, stream, a);
+}
+
+fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void* v4, const void* params,
+                         const int32_t* seqlens, const int32_t* block_table, void* k_out,
+                         void* v_out, fd_stream_t stream) {
+  fd::ExpandArgs a{};
+  const fd_status st = int4_cache(p, k4, v4, params, &a.c);
+  if (st != FD_OK) return st;
+  if (!k_out || !v_out || (p->block_size != 0) != (block_table != nullptr)) return FD_ERR_INVALID_ARGUMENT;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(seqlens, 4) || !aligned(block_table, 4))
+    return FD_ERR_INVALID_ARGUMENT;
+  if (p->max_len == 0) return FD_OK;
+  int dev = 0;
+  const fd_status arch = this_device(&dev);
+  if (arch != FD_OK) return arch;
+  a.seqlens = seqlens;
+  a.block_table = block_table;
+  a.log2_block_size = p->block_size ? ilog2(p->block_size) : 0;
+  a.max_blocks = p->max_blocks_per_seq;
+  a.max_len = p->max_len;
+  a.k = static_cast<__nv_bfloat16*>(k_out);
+  a.v = static_cast<__nv_bfloat16*>(v_out);
+  const dim3 grid(static_cast<unsigned>((p->max_len + fd::kExpandTokens - 1LL) / fd::kExpandTokens),
+                  static_cast<unsigned>(p->Hkv), static_cast<unsigned>(p->B));
+  return p->D == 128 ? launch_chained(fd::fd_expand_int4_kernel<128>, grid, 256, 0, stream, a)
+                     : launch_chained(fd::fd_expand_int4_kernel<64>, grid, 256, 0, stream, a);
+}
+
+fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, const void* v4,
+                         const void* params, const int32_t* seqlens, const int32_t* block_table,
+                         float scale, int num_splits, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, fd_stream_t stream) {
+  fd::Int4DecodeArgs d{};
+  const fd_status st = int4_cache(p, k4, v4, params, &d.c);
+  if (st != FD_OK) return st;
+  if (!q || !out || (p->block_size != 0) != (block_table != nullptr)) return FD_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FD_ERR_INVALID_ARGUMENT;
+  if (num_splits < 1 || num_splits > kMaxSplits) return FD_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
+      !aligned(seqlens, 4) || !aligned(block_table, 4))
+    return FD_ERR_INVALID_ARGUMENT;
+  const Chunking chunks = chunking(p->max_len, num_splits);
+  fd::SplitArgs& a = d.a;
+  if (chunks.splits > 1) {
+    const size_t need = fd_workspace_bytes(p->B, p->Hq, p->D, chunks.splits);
+    if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE;
+    const size_t rows = static_cast<size_t>(p->B) * p->Hq * chunks.splits;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(rows * p->D * 4));
+  }
+  int dev = 0;
+  const fd_status arch = this_device(&dev);
+  if (arch != FD_OK) return arch;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.seqlens = seqlens;
+  a.block_table = block_table;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.G = p->Hq / p->Hkv;
+  a.max_len = p->max_len;
+  a.block_size = p->block_size;
+  a.log2_block_size = p->block_size ? ilog2(p->block_size) : 0;
+  a.max_blocks_per_seq = p->max_blocks_per_seq;
+  a.tiles = chunks.tiles;
+  a.n_splits = chunks.splits;
+  a.tile_q = chunks.tiles / chunks.splits;
+  a.tile_r = chunks.tiles % chunks.splits;
+  a.scale_log2 = scale * 1.4426950408889634074f;
+  a.scale = scale;
+  const dim3 grid(static_cast<unsigned>(chunks.splits), static_cast<unsigned>(p->Hkv),
+                  static_cast<unsigned>(p->B));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  fd_status r = p->D == 128 ? launch_split_int4<128>(d, grid, stream) : launch_split_int4<64>(d, grid, stream);
+  if (r == FD_OK && chunks.splits > 1)
+    r = p->D == 128 ? launch_combine<128>(a, p->B, s) : launch_combine<64>(a, p->B, s);
+  return r;
+}
+
+fd_status fd_alloc_pages(int B, int block_size, int max_blocks_per_seq, int max_tokens,
+                         int num_pages, const int32_t* seqlens, const int32_t* new_lens,
+                         const int32_t* free_pages, const int32_t* free_count,
+                         int32_t* block_table, int32_t* seqlens_out, int32_t* cu_new,
+                         int64_t* slots, int32_t* positions, int32_t* free_count_out,
+                         fd_stream_t stream) {
+  const fd_status st = check_pages(B, block_size, max_blocks_per_seq, num_pages);
+  if (st != FD_OK) return st;
+  if (max_tokens < 0 || !seqlens || !new_lens || !free_pages || !free_count || !block_table ||
+      !seqlens_out || !cu_new || (!slots && max_tokens > 0) || !free_count_out)
+    return FD_ERR_INVALID_ARGUMENT;
+  if (!aligned(seqlens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_count, 4) || !aligned(block_table, 4) || !aligned(seqlens_out, 4) ||
+      !aligned(cu_new, 4) || !aligned(slots, 8) || !aligned(positions, 4) ||
+      !aligned(free_count_out, 4))
+    return FD_ERR_INVALID_ARGUMENT;
+  fd::PageArgs a{};
+  a.B = B;
+  a.log2_block_size = ilog2(block_size);
+  a.max_blocks = max_blocks_per_seq;
+  a.num_pages = num_pages;
+  a.max_items = max_tokens;
+  a.seqlens = seqlens;
+  a.new_lens = new_lens;
+  a.free_pages = const_cast<int32_t*>(free_pages);
+  a.free_count = free_count;
+  a.block_table = block_table;
+  a.seqlens_out = seqlens_out;
+  a.cu_new = cu_new;
+  a.slots = slots;
+  a.positions = positions;
+  a.free_count_out = free_count_out;
+  return launch_pages(fd::fd_alloc_pages_kernel, a, max_tokens, stream);
+}
+
+fd_status fd_release_pages(int B, int block_size, int max_blocks_per_seq, int num_pages,
+                           const int32_t* seqlens, const uint8_t* done,
+                           const int32_t* block_table, int32_t* free_pages,
+                           const int32_t* free_count, int32_t* seqlens_out,
+                           int32_t* free_count_out, fd_stream_t stream) {
+  const fd_status st = check_pages(B, block_size, max_blocks_per_seq, num_pages);
+  if (st != FD_OK) return st;
+  if (!seqlens || !done || !block_table || !free_pages || !free_count || !seqlens_out ||
+      !free_count_out)
+    return FD_ERR_INVALID_ARGUMENT;
+  if (!aligned(seqlens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_count, 4) || !aligned(seqlens_out, 4) || !aligned(free_count_out, 4))
+    return FD_ERR_INVALID_ARGUMENT;
+  fd::PageArgs a{};
+  a.B = B;
+  a.log2_block_size = ilog2(block_size);
+  a.max_blocks = max_blocks_per_seq;
+  a.num_pages = num_pages;
+  a.seqlens = seqlens;
+  a.done = done;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.block_table = const_cast<int32_t*>(block_table);
+  a.seqlens_out = seqlens_out;
+  a.free_count_out = free_count_out;
+  const long long most = std::min<long long>(num_pages, static_cast<long long>(B) * max_blocks_per_seq);
+  return launch_pages(fd::fd_release_pages_kernel, a, most, stream);
+}
+
+}  // extern "C"

@@ -181,127 +181,571 @@ __global__ void __launch_bounds__(256) fd_expand_int4_kernel(const ExpandArgs a)
 // ---------------------------------------------------------------- decode
 
 struct Int4DecodeArgs {
-  SplitArgs a;     // as fd_split_kernel's; k_scale and v_scale do not apply
-  Int4Cache c;
+  SplitArgs a;            // as fd_split_kernel's; k_scale and v_scale do not apply
+  int prefetch_units;     // units per warp pulled into L2 before the wait on the previous grid
 };
 
-constexpr int kInt4Warps = 4;
+// A warp streams units of 32 tokens through a ring of its own: it issues its
+// copies, waits for them and computes, with no other warp to wait for.
+constexpr int kUnit = 32;
+constexpr int kInt4Warps = 8;
+constexpr int kInt4Stages = 3;
+constexpr float kRescaleLog2 = 8.f;   // softmax weights up to 2^8 before a rescale
 
-// The log-sum-exp of a split as the merge takes it.  The merge reads a row
-// whose partials are all NaN as empty; +inf makes it NaN, as NaN rows have to.
-__device__ __forceinline__ float part_lse_of(float lse) { return lse != lse ? INFINITY : lse; }
+// 4-D tile load and L2 prefetch: {byte, head, row, plane}.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, uint32_t bar,
+                                            int head, int row, int plane, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(0), "r"(head), "r"(row), "r"(plane),
+      "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* tm, int head, int row,
+                                                   int plane) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(0), "r"(head), "r"(row), "r"(plane)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+// Nibbles 0, 1 (bits 0-3 and 4-7) of each half of x as f16 pairs c - 8.  A
+// nibble becomes the low mantissa bits of 1024 (or, four bits higher, of 64):
+// one logic operation gives 1024 + c (64 + c), and the subtraction is exact.
+// Products with c - 8 instead of 1024 + c keep the fp32 sums small.
+__device__ __forceinline__ void int4_pair(uint32_t x, uint32_t& n0, uint32_t& n1) {
+  const uint32_t lo = (x & 0x000f000fu) | 0x64006400u;
+  const uint32_t hi = (x & 0x00f000f0u) | 0x54005400u;
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), __half2half2(__ushort_as_half(0x6408)));
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), __half2half2(__ushort_as_half(0x5480)));
+  n0 = *reinterpret_cast<const uint32_t*>(&a);
+  n1 = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <int D, int NB>
+struct Int4Smem {
+  static constexpr int kRowBytes = D / 2;
+  static constexpr int kCodeBytes = kUnit * kRowBytes;
+  static constexpr int kV = kCodeBytes;                 // offsets within a stage
+  static constexpr int kP = 2 * kCodeBytes;
+  static constexpr int kStageBytes = 2 * kCodeBytes + kUnit * 16;
+  static constexpr int kWarpBytes = kInt4Stages * kStageBytes;
+  static constexpr int kBarOffset = kInt4Warps * kWarpBytes;
+  static constexpr int kErrorOffset = kBarOffset + 8 * kInt4Warps * kInt4Stages;
+  static constexpr int kDynamicBytes = kErrorOffset + 16 + 1024;   // room to align to 1 KB
+  // A warp leaves its softmax state in its own drained ring (floats).
+  static constexpr int kNcol = NB * 8;
+  static constexpr int kAccStride = D + 4;
+  static constexpr int kM = kNcol * kAccStride;
+  static constexpr int kL = kM + kNcol;
+  static constexpr int kWarpFloats = kWarpBytes / 4;
+  static_assert(kL + kNcol <= kWarpFloats, "the state of a warp fits its ring");
+};
+
+// Row of a unit's 16-token block that takes slot s (0..7) of the MMAs, 8..15
+// likewise.  A 64-byte code row (D = 128) covers half the banks, chosen by its
+// parity, and its two 32-byte groups lie there as the copy's swizzle puts them,
+// by bit 2 of the row.  The four rows of slots 4i .. 4i+3 (loads of K) and of
+// slots i, i+2, i+4, i+6 (loads of V) are in four different places, so that no
+// load has a bank conflict.  The 32-byte rows of D = 64 need no reordering.
+template <int D>
+__device__ __forceinline__ uint32_t int4_slot_row(uint32_t s) {
+  if constexpr (D == 64) return s;
+  return ((s & 2) << 1) | ((s & 4) >> 1) | ((s ^ (s >> 2)) & 1);
+}
+
+// Address of byte `col` of code row r of a unit; the copy's swizzle (64 bytes
+// for D = 128, 32 for D = 64) exchanges 16-byte chunks.
+template <int D>
+__device__ __forceinline__ uint32_t int4_code_addr(uint32_t base, uint32_t r, uint32_t col) {
+  const uint32_t a = r * (D / 2) + col;
+  if constexpr (D == 128) return base + (a ^ ((r << 3) & 0x30u));
+  return base + (a ^ ((r << 2) & 0x10u));
+}
 
 // Split kernel of a 4-bit cache: one CTA per (split, KV head, sequence), as
-// fd_split_kernel; each warp takes every fourth token, its lanes the entries
-// of the head dimension.
-template <int D, int G>
-__global__ void __launch_bounds__(kInt4Warps * 32) fd_split_int4_kernel(const Int4DecodeArgs p) {
+// fd_split_kernel, with the units of 32 tokens dealt to its warps in turn.
+//
+// Scores.  S^T = (c - 8) q^T on m16n8k16 MMAs (16 tokens by up to 8 heads), one
+// fp32 sum per group of channels; then, per token,
+//   t = ks0 S0 + ks1 S1 + kb0 sum_0(q) + kb1 sum_1(q),
+// so that no scale touches an entry.  q is held in f16 relative to its row's
+// largest entry (a power of two), which keeps the 8 bits of every bf16 entry
+// that is not 2^14 times smaller than the largest.
+// P V.  O^T += (c - 8)^T w on the same MMAs, w = f16(p vs / R) with R a power of
+// two at least as large as every vs the warp has seen (f16's 11 bits; p vs of
+// any size fits), and the biases' part sum_j p_j vb_j in fp32 beside it.
+// A nibble pair costs one logic operation and one subtraction.  V's pairs run
+// along the tokens, so two tokens' words are merged first.
+// The running maximum is only moved when a score passes it by 2^8 (a vote per
+// unit in place of shuffles): weights up to 2^8 until then.
+template <int D, int NB>
+__global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
+    fd_split_int4_kernel(const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ CUtensorMap tmP, const Int4DecodeArgs p) {
+  using L = Int4Smem<D, NB>;
+  constexpr int KS = D / 32;          // k-steps of a group's score MMA
+  constexpr int MB = D / 32;          // m-blocks of a group's P V MMA
   const SplitArgs& a = p.a;
-  grid_dependency_wait();
-  constexpr int VPL = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = seq_length(a.seqlens, b, a.max_len);
+  const int g = lane >> 2, t4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * L::kWarpBytes;
+  const uint32_t bar = smem_u32(smem) + L::kBarOffset + 8 * kInt4Stages * warp;
+  volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);
   const int start = split_first_tile(a, split) * kTile;
-  const int end = min(split_first_tile(a, split + 1) * kTile, n);
-  const int h0 = kvh * G;
+  const int split_end = split_first_tile(a, split + 1) * kTile;
+
+  if (lane == 0) {
+    for (int s = 0; s < kInt4Stages; ++s) mbar_init(bar + 8 * s, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    prefetch_tensormap(&tmP);
+  }
+  if (threadIdx.x == 0) *cta_error = 0;
+  if (lane < p.prefetch_units) {
+    // Only kernel arguments are used: the lengths may still be in flight.
+    const int t0 = start + (warp + lane * kInt4Warps) * kUnit;
+    if (t0 < min(split_end, a.max_len)) {
+      tma_prefetch_l2_4d(&tmK, kvh, t0, b);
+      tma_prefetch_l2_4d(&tmV, kvh, t0, b);
+      tma_prefetch_l2_4d(&tmP, kvh, t0, b);
+    }
+  }
+  __syncthreads();
+  grid_dependency_wait();
+
+  const int n = seq_length(a.seqlens, b, a.max_len);
+  const int end = min(split_end, n);
+  const int h0 = kvh * a.G;
   const int n_parts = (a.n_splits == 1 || (n + kTile - 1) / kTile <= a.tile_q) ? 1 : 2;
   if (start >= end) {
-    grid_dependents_launch();
-    if (split == 0) {
+    if (split == 0) {   // an empty sequence
       const size_t base = (static_cast<size_t>(b) * a.Hq + h0) * D;
-      for (int i = threadIdx.x; i < G * D; i += kInt4Warps * 32) a.out[base + i] = __float2bfloat16_rn(0.f);
-      if (a.lse && threadIdx.x < G) a.lse[static_cast<size_t>(b) * a.Hq + h0 + threadIdx.x] = -INFINITY;
+      for (int i = threadIdx.x; i < a.G * D; i += kInt4Warps * 32) a.out[base + i] = __float2bfloat16_rn(0.f);
+      if (a.lse && threadIdx.x < a.G) a.lse[static_cast<size_t>(b) * a.Hq + h0 + threadIdx.x] = -INFINITY;
     }
     return;
   }
-  float q[G][VPL], acc[G][VPL], m[G], l[G];
+  const int n_units = (end - start + kUnit - 1) / kUnit;
+  const int mine = warp < n_units ? (n_units - warp + kInt4Warps - 1) / kInt4Warps : 0;
+
+  // ---- copies: unit i of this warp holds tokens start + 32 (warp + 8 i) ..
+  const uint64_t policy = policy_evict_first();
+  const bool paged = a.block_size != 0;
+  const int lbs = a.log2_block_size;
+  const int pages_per_unit = paged && a.block_size < kUnit ? kUnit >> lbs : 1;
+  const int box_rows = kUnit / pages_per_unit;
+  const int n_pages = paged ? (n + a.block_size - 1) >> lbs : 0;
+  const int32_t* table = a.block_table + static_cast<size_t>(b) * a.max_blocks_per_seq;
+  auto unit_token = [&](int i) { return start + (warp + i * kInt4Warps) * kUnit; };
+  // The page of this lane's box in unit i (lanes past the boxes: none).
+  auto page_of = [&](int i) {
+    const int pg = (unit_token(i) >> lbs) + lane;
+    return paged && i < mine && lane < pages_per_unit && pg < n_pages ? __ldg(table + pg) : 0;
+  };
+  int next_page = page_of(0);
+  auto issue = [&](int i) {
+    const int t0 = unit_token(i);
+    const uint32_t st = ring + (i % kInt4Stages) * L::kStageBytes;
+    const uint32_t full = bar + 8 * (i % kInt4Stages);
+    const int boxes = paged ? min(pages_per_unit, n_pages - (t0 >> lbs)) : 1;
+    if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (D + 16));
+    __syncwarp();
+    if (lane < boxes) {
+      const int plane = paged ? next_page : b;
+      const int row = paged ? (t0 & (a.block_size - 1)) : t0;
+      const uint32_t r = lane * box_rows;
+      tma_load_4d(st + r * L::kRowBytes, &tmK, full, kvh, row, plane, policy);
+      tma_load_4d(st + L::kV + r * L::kRowBytes, &tmV, full, kvh, row, plane, policy);
+      tma_load_4d(st + L::kP + r * 16, &tmP, full, kvh, row, plane, policy);
+    }
+    next_page = page_of(i + 1);
+  };
+  int issued = 0;
+  for (; issued < min(mine, kInt4Stages); ++issued) issue(issued);
+
+  // ---- q: f16 relative to the head's largest entry, in the order of K's
+  // codes: word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
+  uint32_t qf[NB][2][KS][2];
+  float sq[NB][2][2], scl[NB][2];      // per column 2 t4 + c: sum of q per group, scale
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
+  for (int nb = 0; nb < NB; ++nb) {
+    const bool live = nb * 8 + g < a.G;
+    const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(b) * a.Hq + h0 + (live ? nb * 8 + g : 0)) * D;
+    uint4 raw[2][KS / 2];
+    float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      q[g][i] = __bfloat162float(a.q[(static_cast<size_t>(b) * a.Hq + h0 + g) * D + lane * VPL + i]);
-      acc[g][i] = 0.f;
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < KS / 2; ++w) {
+        raw[h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
+        const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int e = 0;
+    if (live && mx <= 3.4e38f) frexpf(mx, &e);        // mx = f 2^e, f in [0.5, 1); 0 for 0
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < KS / 2; ++w) {
+        const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
+        __half y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = live ? ldexpf((i & 1) ? bf16_hi(x[i / 2]) : bf16_lo(x[i / 2]), -e) : 0.f;
+          y[i] = __float2half_rn(f);
+          sum[h] += __half2float(y[i]);
+        }
+        // k-step 2w + s: slots 2t, 2t+1 are nibbles 2s, 2s+4, slots 2t+8, 2t+9
+        // nibbles 2s+1, 2s+5 (the pairs that one mask leaves).
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 v = __halves2half2(y[2 * s + i], y[2 * s + i + 4]);
+            qf[nb][h][2 * w + s][i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+    }
+    const float sc = ldexpf(a.scale_log2, e);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int from = 8 * t4 + 4 * c;                // a lane of head 2 t4 + c
+      sq[nb][0][c] = __shfl_sync(0xffffffffu, sum[0], from);
+      sq[nb][1][c] = __shfl_sync(0xffffffffu, sum[1], from);
+      scl[nb][c] = __shfl_sync(0xffffffffu, sc, from);
     }
   }
-  for (int t = start + warp; t < end; t += kInt4Warps) {
-    int plane = b, row = t;
-    if (a.block_table) {
-      plane = a.block_table[static_cast<size_t>(b) * a.max_blocks_per_seq + (t >> a.log2_block_size)];
-      row = t & (a.block_size - 1);
+
+  // ---- softmax state.  Per column: the reference m (in units of t), m scl as
+  // it enters the weights, and the t beyond which it moves.
+  float m_ref[NB][2], m_log2[NB][2], bound[NB][2], l_run[NB][2], bias[NB][2][2];
+  float acc[NB][2][MB][4];
+  float inv_r[2] = {0x1p126f, 0x1p126f};              // 1 / R per group
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      m_ref[nb][c] = bound[nb][c] = -INFINITY;
+      m_log2[nb][c] = l_run[nb][c] = bias[nb][0][c] = bias[nb][1][c] = 0.f;
     }
-    float k[VPL], v[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) k[i] = v[i] = 0.f;
-    if (plane >= 0 && plane < p.c.planes) {
-      const size_t from = int4_row(p.c, plane, kvh, row);
-      const uint32_t* rec = reinterpret_cast<const uint32_t*>(p.c.params + from * 16) + lane / 16;
-      const uint32_t kr = rec[0], vr = rec[2];
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < VPL; i += 2) {
-        const uint32_t kc = p.c.k4[from * (D / 2) + (lane * VPL + i) / 2];
-        const uint32_t vc = p.c.v4[from * (D / 2) + (lane * VPL + i) / 2];
-        k[i] = __fmaf_rn(bf16_lo(kr), static_cast<float>(static_cast<int>(kc & 15u) - 8), bf16_hi(kr));
-        k[i + 1] = __fmaf_rn(bf16_lo(kr), static_cast<float>(static_cast<int>(kc >> 4) - 8), bf16_hi(kr));
-        v[i] = __fmaf_rn(bf16_lo(vr), static_cast<float>(static_cast<int>(vc & 15u) - 8), bf16_hi(vr));
-        v[i + 1] = __fmaf_rn(bf16_lo(vr), static_cast<float>(static_cast<int>(vc >> 4) - 8), bf16_hi(vr));
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nb][h][j][i] = 0.f;
+
+  const uint32_t k_row = int4_slot_row<D>(g);          // and k_row + 8
+  bool failed = false;
+  for (int i = 0; i < mine; ++i) {
+    const uint32_t st = ring + (i % kInt4Stages) * L::kStageBytes;
+    const bool ok = mbar_wait(bar + 8 * (i % kInt4Stages), (i / kInt4Stages) & 1, kWaitLimitNs);
+    if (!__all_sync(0xffffffffu, ok)) {
+      failed = true;
+      break;
+    }
+    const int valid = end - unit_token(i);             // tokens of the unit that count
+
+    // Records of this lane's four tokens: block bb, slots g and g + 8.
+    uint4 rec[2][2];
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        rec[bb][r] = lds128(st + L::kP + (16 * bb + 8 * r + k_row) * 16);
+        if (valid < kUnit && 16 * bb + 8 * r + static_cast<int>(k_row) >= valid)
+          rec[bb][r] = make_uint4(0u, 0u, 0u, 0u);
+      }
+
+    // Scores, t[bb][row][column].
+    float t[NB][2][2][2];
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb) {
+      float sc[NB][2][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[nb][h][x] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[2][KS / 2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t at = int4_code_addr<D>(st, 16 * bb + 8 * r + k_row, h * (D / 4) + t4 * (D / 16));
+          if constexpr (D == 128) {
+            const uint2 v = lds64(at);
+            w[r][0] = v.x;
+            w[r][1] = v.y;
+          } else {
+            w[r][0] = lds32(at);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t af[4];
+          int4_pair(w[0][k / 2] >> (8 * (k & 1)), af[0], af[2]);
+          int4_pair(w[1][k / 2] >> (8 * (k & 1)), af[1], af[3]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = bf16_hi(rec[bb][r].x) * sq[nb][0][c];
+            x = fmaf(bf16_hi(rec[bb][r].y), sq[nb][1][c], x);
+            x = fmaf(bf16_lo(rec[bb][r].x), sc[nb][0][2 * r + c], x);
+            x = fmaf(bf16_lo(rec[bb][r].y), sc[nb][1][2 * r + c], x);
+            t[nb][bb][r][c] = x;
+          }
+    }
+    if (valid < kUnit) {
+#pragma unroll
+      for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (16 * bb + 8 * r + static_cast<int>(k_row) >= valid) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) t[nb][bb][r][0] = t[nb][bb][r][1] = -INFINITY;
+          }
+    }
+
+    // Does a score pass its bound, or a V scale R?
+    float top[NB][2], vtop[2];
+    bool move = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        top[nb][c] = fmaxf(fmaxf(t[nb][0][0][c], t[nb][0][1][c]), fmaxf(t[nb][1][0][c], t[nb][1][1][c]));
+        move |= top[nb][c] > bound[nb][c];
+      }
+    vtop[0] = vtop[1] = 0.f;
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        vtop[0] = fmaxf(vtop[0], fabsf(bf16_lo(rec[bb][r].z)));
+        vtop[1] = fmaxf(vtop[1], fabsf(bf16_lo(rec[bb][r].w)));
+      }
+    move |= vtop[0] * inv_r[0] > 1.f || vtop[1] * inv_r[1] > 1.f;
+    if (__any_sync(0xffffffffu, move)) {
+      float keep_r[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) vtop[h] = fmaxf(vtop[h], __shfl_xor_sync(0xffffffffu, vtop[h], off));
+        keep_r[h] = 1.f;
+        if (vtop[h] * inv_r[h] > 1.f) {
+          int e;
+          frexpf(vtop[h], &e);                        // vtop < 2^e, e <= 126 as vs < 2^126
+          const float r = ldexpf(1.f, -max(e, -126));
+          keep_r[h] = r / inv_r[h];                   // old R / new R; 0 from the initial 2^-126
+          inv_r[h] = r;
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            top[nb][c] = fmaxf(top[nb][c], __shfl_xor_sync(0xffffffffu, top[nb][c], off));
+          const float m = fmaxf(m_ref[nb][c], top[nb][c]);
+          const float ml = m == -INFINITY ? 0.f : m * scl[nb][c];
+          const float al = m_ref[nb][c] == -INFINITY ? 0.f : ex2(m_log2[nb][c] - ml);
+          m_ref[nb][c] = m;
+          m_log2[nb][c] = ml;
+          if (m != -INFINITY) bound[nb][c] = m + fminf(kRescaleLog2 / scl[nb][c], 3e38f);
+          l_run[nb][c] *= al;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bias[nb][h][c] *= al;
+#pragma unroll
+            for (int j = 0; j < MB; ++j) {
+              acc[nb][h][j][c] *= al * keep_r[h];
+              acc[nb][h][j][c + 2] *= al * keep_r[h];
+            }
+          }
+        }
+    }
+
+    // Weights, and P V for the 16 tokens of each block.
+#pragma unroll
+    for (int bb = 0; bb < 2; ++bb) {
+      uint32_t pb[NB][2][2];       // [group][slots 0-7, 8-15]
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float vs[2] = {bf16_lo(rec[bb][r].z) * inv_r[0], bf16_lo(rec[bb][r].w) * inv_r[1]};
+        const float vb[2] = {bf16_hi(rec[bb][r].z), bf16_hi(rec[bb][r].w)};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float e[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], -m_log2[nb][c]));
+            l_run[nb][c] += e[c];
+            bias[nb][0][c] = fmaf(e[c], vb[0], bias[nb][0][c]);
+            bias[nb][1][c] = fmaf(e[c], vb[1], bias[nb][1][c]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) pb[nb][h][r] = movmatrix_trans(pack_f16x2(e[0] * vs[h], e[1] * vs[h]));
+        }
+      }
+      // Slots 2 t4, 2 t4 + 1 and 8 more: this lane's tokens in V.
+      const uint32_t v0 = 16 * bb + int4_slot_row<D>(2 * t4), v1 = 16 * bb + int4_slot_row<D>(2 * t4 + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[2][2];          // [slots 0-7, 8-15][low, high half of the words]: two tokens' halves
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t a0 = int4_code_addr<D>(st + L::kV, v0 + 8 * r, h * (D / 4) + g * (D / 32));
+          const uint32_t a1 = int4_code_addr<D>(st + L::kV, v1 + 8 * r, h * (D / 4) + g * (D / 32));
+          if constexpr (D == 128) {
+            const uint32_t w0 = lds32(a0), w1 = lds32(a1);
+            x[r][0] = __byte_perm(w0, w1, 0x5410);
+            x[r][1] = __byte_perm(w0, w1, 0x7632);
+          } else {
+            x[r][0] = __byte_perm(lds16(a0), lds16(a1), 0x5410);
+            x[r][1] = 0u;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          uint32_t vf[4];
+          int4_pair(x[0][j / 2] >> (8 * (j & 1)), vf[0], vf[1]);
+          int4_pair(x[1][j / 2] >> (8 * (j & 1)), vf[2], vf[3]);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(acc[nb][h][j], vf, pb[nb][h][0], pb[nb][h][1]);
+        }
       }
     }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) s += q[g][i] * k[i];
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m[g], s);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const float al = ex2(m[g] - mu), e = ex2(s - mu);
-      m[g] = mn;
-      l[g] = l[g] * al + e;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[g][i] = acc[g][i] * al + e * v[i];
-    }
+    __syncwarp();
+    if (issued < mine) issue(issued++);
   }
   grid_dependents_launch();
-  // Merge of the warps' states.
-  __shared__ float s_m[kInt4Warps][G], s_l[kInt4Warps][G], s_o[kInt4Warps][D];
-  if (lane == 0) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      s_m[warp][g] = m[g];
-      s_l[warp][g] = l[g];
-    }
+  if (failed && lane == 0) {
+    raise_device_error(1u);
+    *cta_error = 1;
+    // No copy may still be landing in shared memory when the CTA retires.
+    for (int i = issued > kInt4Stages ? issued - kInt4Stages : 0; i < issued; ++i)
+      if (!mbar_wait(bar + 8 * (i % kInt4Stages), (i / kInt4Stages) & 1, kWaitLimitNs)) raise_device_error(2u);
   }
+  __syncwarp();
+
+  // ---- merge of the warps' states.  Row g of m-block j of group h is entry
+  // h D/2 + g D/16 + 2 j, row g + 8 the next one.
+  float* f = reinterpret_cast<float*>(smem) + warp * L::kWarpFloats;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s_o[warp][lane * VPL + i] = acc[g][i];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f, o = 0.f;
-    const int d = threadIdx.x;
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-    for (int w = 0; w < kInt4Warps; ++w) M = fmaxf(M, s_m[w][g]);
-    const float mu = M == -INFINITY ? 0.f : M;
+      for (int off = 4; off < 32; off <<= 1) {
+        l_run[nb][c] += __shfl_xor_sync(0xffffffffu, l_run[nb][c], off);
+        bias[nb][0][c] += __shfl_xor_sync(0xffffffffu, bias[nb][0][c], off);
+        bias[nb][1][c] += __shfl_xor_sync(0xffffffffu, bias[nb][1][c], off);
+      }
+      const int col = nb * 8 + 2 * t4 + c;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float r = 1.f / inv_r[h];
+        float* o = f + col * L::kAccStride + h * (D / 2) + g * (D / 16);
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+          *reinterpret_cast<float2*>(o + 2 * j) =
+              make_float2(fmaf(acc[nb][h][j][c], r, bias[nb][h][c]), fmaf(acc[nb][h][j][c + 2], r, bias[nb][h][c]));
+      }
+      if (g == 0) {
+        f[L::kM + col] = m_ref[nb][c] == -INFINITY && l_run[nb][c] == 0.f ? -INFINITY : m_log2[nb][c];
+        f[L::kL + col] = l_run[nb][c];
+      }
+    }
+  __syncthreads();
+  if (*cta_error) return;
+  const float* all = reinterpret_cast<const float*>(smem);
+  constexpr int kChunks = D / 4;
+  for (int c = threadIdx.x; c < a.G * kChunks; c += kInt4Warps * 32) {
+    const int hd = c / kChunks, d = (c % kChunks) * 4;
+    float m[kInt4Warps], M = -INFINITY, l = 0.f;
 #pragma unroll
     for (int w = 0; w < kInt4Warps; ++w) {
-      const float wt = ex2(s_m[w][g] - mu);
-      L += wt * s_l[w][g];
-      if (d < D) o += wt * s_o[w][d];
+      m[w] = all[w * L::kWarpFloats + L::kM + hd];
+      M = fmaxf(M, m[w]);
     }
-    const size_t r = static_cast<size_t>(b) * a.Hq + h0 + g;
-    const float lse = (M + log2f(L)) * 0.69314718055994530942f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kInt4Warps; ++w) {
+      if (m[w] == -INFINITY) continue;                 // no token
+      const float wt = ex2(m[w] - M);
+      const float4 v = *reinterpret_cast<const float4*>(all + w * L::kWarpFloats + hd * L::kAccStride + d);
+      l += wt * all[w * L::kWarpFloats + L::kL + hd];
+      o.x += wt * v.x;
+      o.y += wt * v.y;
+      o.z += wt * v.z;
+      o.w += wt * v.w;
+    }
+    const float inv = 1.f / l;
+    const float lse = (M + log2f(l)) * 0.69314718055994530942f;
+    const size_t row = static_cast<size_t>(b) * a.Hq + h0 + hd;
     if (n_parts == 1) {
-      if (d < D) a.out[r * D + d] = __float2bfloat16_rn(o / L);
-      if (a.lse && d == 0) a.lse[r] = lse;
+      *reinterpret_cast<uint2*>(a.out + row * D + d) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (d == 0 && a.lse) a.lse[row] = lse;
     } else {
-      if (d < D) a.part_o[(r * a.n_splits + split) * D + d] = o / L;
-      if (d == 0) a.part_lse[r * a.n_splits + split] = part_lse_of(lse);
+      *reinterpret_cast<float4*>(a.part_o + (row * a.n_splits + split) * D + d) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      // The merge takes a row whose partials are all NaN as empty; +inf makes
+      // it NaN, as rows of NaN have to.
+      if (d == 0) a.part_lse[row * a.n_splits + split] = lse != lse ? INFINITY : lse;
     }
-    __syncthreads();
   }
 }
 

@@ -53,16 +53,73 @@ fd_status launch_chained(Kernel kernel, dim3 grid, int threads, size_t smem, fd_
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
-template <int D>
-fd_status launch_split_int4(const fd::Int4DecodeArgs& a, dim3 grid, fd_stream_t s) {
-  const int threads = fd::kInt4Warps * 32;
-  switch (a.a.G) {
-    case 1: return launch_chained(fd::fd_split_int4_kernel<D, 1>, grid, threads, 0, s, a);
-    case 2: return launch_chained(fd::fd_split_int4_kernel<D, 2>, grid, threads, 0, s, a);
-    case 4: return launch_chained(fd::fd_split_int4_kernel<D, 4>, grid, threads, 0, s, a);
-    case 8: return launch_chained(fd::fd_split_int4_kernel<D, 8>, grid, threads, 0, s, a);
-    default: return launch_chained(fd::fd_split_int4_kernel<D, 16>, grid, threads, 0, s, a);
+// Tensor maps of a 4-bit cache, {byte, head, row, plane}: the codes of K and of
+// V (a box row is a whole code row, swizzled over its own width) and the
+// records (16 bytes a box row).  Coordinates outside the cache read zeros.
+struct Int4Maps {
+  CUtensorMap k, v, p;
+};
+
+fd_status make_int4_map(CUtensorMap* tm, const void* base, int row_bytes, const fd::Int4Cache& c,
+                        int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (encoder(&enc) != FD_OK) return FD_ERR_CUDA;
+  const cuuint64_t rb = static_cast<cuuint64_t>(row_bytes), rows = static_cast<cuuint64_t>(std::max(c.rows, 1));
+  cuuint64_t dims[4] = {rb, static_cast<cuuint64_t>(c.Hkv), rows, static_cast<cuuint64_t>(c.planes)};
+  cuuint64_t strides[3] = {c.nhd ? rb : rows * rb, c.nhd ? c.Hkv * rb : rb, c.Hkv * rows * rb};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(row_bytes), 1, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle swizzle = row_bytes == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : row_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                       : CU_TENSOR_MAP_SWIZZLE_NONE;
+  const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides,
+                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FD_OK : FD_ERR_CUDA;
+}
+
+// The maps depend only on addresses, shape and device: each host thread keeps
+// the last few it encoded, as cached_cache_map does.
+fd_status cached_int4_maps(Int4Maps* m, const fd::Int4Cache& c, int D, int box_rows, int dev) {
+  struct Entry {
+    fd::Int4Cache c;
+    int D, box_rows, dev;
+    Int4Maps maps;
+  };
+  constexpr int kEntries = 8;
+  thread_local Entry entries[kEntries] = {};
+  thread_local int next = 0;
+  for (const Entry& e : entries) {
+    if (e.D == D && e.box_rows == box_rows && e.dev == dev && e.c.k4 == c.k4 && e.c.v4 == c.v4 &&
+        e.c.params == c.params && e.c.planes == c.planes && e.c.rows == c.rows && e.c.Hkv == c.Hkv &&
+        e.c.nhd == c.nhd) {
+      *m = e.maps;
+      return FD_OK;
+    }
   }
+  if (make_int4_map(&m->k, c.k4, D / 2, c, box_rows) != FD_OK ||
+      make_int4_map(&m->v, c.v4, D / 2, c, box_rows) != FD_OK ||
+      make_int4_map(&m->p, c.params, 16, c, box_rows) != FD_OK)
+    return FD_ERR_CUDA;
+  entries[next] = Entry{c, D, box_rows, dev, *m};
+  next = (next + 1) % kEntries;
+  return FD_OK;
+}
+
+template <int D, int NB>
+fd_status launch_split_int4(const Int4Maps& m, const fd::Int4DecodeArgs& a, dim3 grid, int dev,
+                            fd_stream_t s) {
+  using L = fd::Int4Smem<D, NB>;
+  auto kern = fd::fd_split_int4_kernel<D, NB>;
+  static std::atomic<unsigned long long> attr_ctx[kMaxDevices];   // as launch_split's
+  const unsigned long long ctx = current_context_id();
+  if (ctx == 0 || attr_ctx[dev].load() != ctx) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L::kDynamicBytes) != cudaSuccess)
+      return FD_ERR_CUDA;
+    attr_ctx[dev].store(ctx);
+  }
+  return launch_chained(kern, grid, fd::kInt4Warps * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
 }
 
 // Do two arrays of int32 share memory?
@@ -169,7 +226,8 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
                          float scale, int num_splits, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, fd_stream_t stream) {
   fd::Int4DecodeArgs d{};
-  const fd_status st = int4_cache(p, k4, v4, params, &d.c);
+  fd::Int4Cache c;
+  const fd_status st = int4_cache(p, k4, v4, params, &c);
   if (st != FD_OK) return st;
   if (!q || !out || (p->block_size != 0) != (block_table != nullptr)) return FD_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FD_ERR_INVALID_ARGUMENT;
@@ -189,6 +247,9 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   int dev = 0;
   const fd_status arch = this_device(&dev);
   if (arch != FD_OK) return arch;
+  Int4Maps maps;
+  const int box_rows = p->block_size ? std::min(p->block_size, fd::kUnit) : fd::kUnit;
+  if (cached_int4_maps(&maps, c, p->D, box_rows, dev) != FD_OK) return FD_ERR_CUDA;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.seqlens = seqlens;
   a.block_table = block_table;
@@ -207,10 +268,17 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.tile_r = chunks.tiles % chunks.splits;
   a.scale_log2 = scale * 1.4426950408889634074f;
   a.scale = scale;
+  d.prefetch_units = p->block_size ? 0 : fd::kInt4Stages;
   const dim3 grid(static_cast<unsigned>(chunks.splits), static_cast<unsigned>(p->Hkv),
                   static_cast<unsigned>(p->B));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  fd_status r = p->D == 128 ? launch_split_int4<128>(d, grid, stream) : launch_split_int4<64>(d, grid, stream);
+  fd_status r;
+  if (p->D == 128)
+    r = a.G <= 8 ? launch_split_int4<128, 1>(maps, d, grid, dev, stream)
+                 : launch_split_int4<128, 2>(maps, d, grid, dev, stream);
+  else
+    r = a.G <= 8 ? launch_split_int4<64, 1>(maps, d, grid, dev, stream)
+                 : launch_split_int4<64, 2>(maps, d, grid, dev, stream);
   if (r == FD_OK && chunks.splits > 1)
     r = p->D == 128 ? launch_combine<128>(a, p->B, s) : launch_combine<64>(a, p->B, s);
   return r;

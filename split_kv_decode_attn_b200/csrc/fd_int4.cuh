@@ -180,11 +180,6 @@ __global__ void __launch_bounds__(256) fd_expand_int4_kernel(const ExpandArgs a)
 
 // ---------------------------------------------------------------- decode
 
-struct Int4DecodeArgs {
-  SplitArgs a;            // as fd_split_kernel's; k_scale and v_scale do not apply
-  int prefetch_units;     // units per warp pulled into L2 before the wait on the previous grid
-};
-
 // A warp streams units of 32 tokens through a ring of its own: it issues its
 // copies, waits for them and computes, with no other warp to wait for.
 constexpr int kUnit = 32;
@@ -211,36 +206,47 @@ __device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* tm, int he
                : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
+// D = A B with a zero accumulator (m16n8k16, f16 inputs, fp32 result).
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t (&a)[4],
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Nibbles 0, 1 (bits 0-3 and 4-7) of each half of x as f16 pairs c - 8.  A
-// nibble becomes the low mantissa bits of 1024 (or, four bits higher, of 64):
-// one logic operation gives 1024 + c (64 + c), and the subtraction is exact.
-// Products with c - 8 instead of 1024 + c keep the fp32 sums small.
-__device__ __forceinline__ void int4_pair(uint32_t x, uint32_t& n0, uint32_t& n1) {
-  const uint32_t lo = (x & 0x000f000fu) | 0x64006400u;
-  const uint32_t hi = (x & 0x00f000f0u) | 0x54005400u;
+template <class T>
+__device__ __forceinline__ T smem_at(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
+}
+
+// (x & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+
+// Exponents that turn a nibble into an f16 number: 1024 + c with the nibble in
+// the low mantissa bits, 64 + c with it four bits higher.  They come in as
+// kernel arguments: as constants the compiler spends a second instruction per
+// pair on them (one logic operation takes one immediate).
+struct Int4Magic {
+  uint32_t k1024, k64;       // 0x64006400, 0x54005400
+};
+
+struct Int4DecodeArgs {
+  SplitArgs a;            // as fd_split_kernel's; k_scale and v_scale do not apply
+  Int4Magic magic;
+  int prefetch_units;     // units per warp pulled into L2 before the wait on the previous grid
+};
+
+// Nibbles 0, 1 (bits 0-3 and 4-7) of each half of x as f16 pairs c - 8.  The
+// subtraction is exact, and products with c - 8 instead of 1024 + c keep the
+// fp32 sums small.
+__device__ __forceinline__ void int4_pair(const Int4Magic& mg, uint32_t x, uint32_t& n0, uint32_t& n1) {
+  const uint32_t lo = and_or(x, 0x000f000fu, mg.k1024), hi = and_or(x, 0x00f000f0u, mg.k64);
   const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), __half2half2(__ushort_as_half(0x6408)));
   const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), __half2half2(__ushort_as_half(0x5480)));
   n0 = *reinterpret_cast<const uint32_t*>(&a);
@@ -279,13 +285,13 @@ __device__ __forceinline__ uint32_t int4_slot_row(uint32_t s) {
   return ((s & 2) << 1) | ((s & 4) >> 1) | ((s ^ (s >> 2)) & 1);
 }
 
-// Address of byte `col` of code row r of a unit; the copy's swizzle (64 bytes
-// for D = 128, 32 for D = 64) exchanges 16-byte chunks.
+// Offset of byte `col` of code row r (0..7) of a unit; the copy's swizzle (64
+// bytes for D = 128, 32 for D = 64) exchanges 16-byte chunks and repeats every
+// 8 rows, so that rows r + 8 i are i * kEightRows further.
 template <int D>
-__device__ __forceinline__ uint32_t int4_code_addr(uint32_t base, uint32_t r, uint32_t col) {
+__device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
   const uint32_t a = r * (D / 2) + col;
-  if constexpr (D == 128) return base + (a ^ ((r << 3) & 0x30u));
-  return base + (a ^ ((r << 2) & 0x10u));
+  return D == 128 ? a ^ ((r << 3) & 0x30u) : a ^ ((r << 2) & 0x10u);
 }
 
 // Split kernel of a 4-bit cache: one CTA per (split, KV head, sequence), as
@@ -319,7 +325,8 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * L::kWarpBytes;
+  uint8_t* ring = smem + warp * L::kWarpBytes;
+  const uint32_t ring_at = smem_u32(ring);
   const uint32_t bar = smem_u32(smem) + L::kBarOffset + 8 * kInt4Stages * warp;
   volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);
   const int start = split_first_tile(a, split) * kTile;
@@ -375,25 +382,33 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     return paged && i < mine && lane < pages_per_unit && pg < n_pages ? __ldg(table + pg) : 0;
   };
   int next_page = page_of(0);
-  auto issue = [&](int i) {
+  auto issue = [&](int i, uint32_t s) {                // into stage s
     const int t0 = unit_token(i);
-    const uint32_t st = ring + (i % kInt4Stages) * L::kStageBytes;
-    const uint32_t full = bar + 8 * (i % kInt4Stages);
-    const int boxes = paged ? min(pages_per_unit, n_pages - (t0 >> lbs)) : 1;
-    if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (D + 16));
-    __syncwarp();
-    if (lane < boxes) {
-      const int plane = paged ? next_page : b;
-      const int row = paged ? (t0 & (a.block_size - 1)) : t0;
-      const uint32_t r = lane * box_rows;
-      tma_load_4d(st + r * L::kRowBytes, &tmK, full, kvh, row, plane, policy);
-      tma_load_4d(st + L::kV + r * L::kRowBytes, &tmV, full, kvh, row, plane, policy);
-      tma_load_4d(st + L::kP + r * 16, &tmP, full, kvh, row, plane, policy);
+    const uint32_t st = ring_at + s * L::kStageBytes;
+    const uint32_t full = bar + 8 * s;
+    if (!paged) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full, kUnit * (D + 16));
+        tma_load_4d(st, &tmK, full, kvh, t0, b, policy);
+        tma_load_4d(st + L::kV, &tmV, full, kvh, t0, b, policy);
+        tma_load_4d(st + L::kP, &tmP, full, kvh, t0, b, policy);
+      }
+    } else {
+      const int boxes = min(pages_per_unit, n_pages - (t0 >> lbs));
+      if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (D + 16));
+      __syncwarp();
+      if (lane < boxes) {
+        const int row = t0 & (a.block_size - 1);
+        const uint32_t r = lane * box_rows;
+        tma_load_4d(st + r * L::kRowBytes, &tmK, full, kvh, row, next_page, policy);
+        tma_load_4d(st + L::kV + r * L::kRowBytes, &tmV, full, kvh, row, next_page, policy);
+        tma_load_4d(st + L::kP + r * 16, &tmP, full, kvh, row, next_page, policy);
+      }
+      next_page = page_of(i + 1);
     }
-    next_page = page_of(i + 1);
   };
   int issued = 0;
-  for (; issued < min(mine, kInt4Stages); ++issued) issue(issued);
+  for (; issued < min(mine, kInt4Stages); ++issued) issue(issued, issued);
 
   // ---- q: f16 relative to the head's largest entry, in the order of K's
   // codes: word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
@@ -477,11 +492,24 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nb][h][j][i] = 0.f;
 
-  const uint32_t k_row = int4_slot_row<D>(g);          // and k_row + 8
+  // Offsets within a unit of this lane's loads: codes of K (slot g), of V
+  // (slots 2 t4 and 2 t4 + 1) and the record of slot g.
+  constexpr uint32_t kEight = 8 * L::kRowBytes;        // 8 rows further
+  const uint32_t k_row = int4_slot_row<D>(g);
+  uint32_t k_at[2], v_at[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    k_at[h] = int4_code_offset<D>(k_row, h * (D / 4) + t4 * (D / 16));
+    v_at[h][0] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4), h * (D / 4) + g * (D / 32));
+    v_at[h][1] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4 + 1), h * (D / 4) + g * (D / 32));
+  }
+  const uint32_t p_at = L::kP + k_row * 16;
+  const Int4Magic mg = p.magic;
   bool failed = false;
+  uint32_t stage = 0, phase = 0;
   for (int i = 0; i < mine; ++i) {
-    const uint32_t st = ring + (i % kInt4Stages) * L::kStageBytes;
-    const bool ok = mbar_wait(bar + 8 * (i % kInt4Stages), (i / kInt4Stages) & 1, kWaitLimitNs);
+    const uint8_t* st = ring + stage * L::kStageBytes;
+    const bool ok = mbar_wait(bar + 8 * stage, phase, kWaitLimitNs);
     if (!__all_sync(0xffffffffu, ok)) {
       failed = true;
       break;
@@ -493,11 +521,14 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
     for (int bb = 0; bb < 2; ++bb)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        rec[bb][r] = lds128(st + L::kP + (16 * bb + 8 * r + k_row) * 16);
-        if (valid < kUnit && 16 * bb + 8 * r + static_cast<int>(k_row) >= valid)
-          rec[bb][r] = make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int r = 0; r < 2; ++r) rec[bb][r] = smem_at<uint4>(st + p_at + (16 * bb + 8 * r) * 16);
+    if (valid < kUnit) {
+#pragma unroll
+      for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (16 * bb + 8 * r + static_cast<int>(k_row) >= valid) rec[bb][r] = make_uint4(0u, 0u, 0u, 0u);
+    }
 
     // Scores, t[bb][row][column].
     float t[NB][2][2][2];
@@ -505,32 +536,31 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     for (int bb = 0; bb < 2; ++bb) {
       float sc[NB][2][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[nb][h][x] = 0.f;
-#pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[2][KS / 2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t at = int4_code_addr<D>(st, 16 * bb + 8 * r + k_row, h * (D / 4) + t4 * (D / 16));
+          const uint8_t* at = st + k_at[h] + (2 * bb + r) * kEight;
           if constexpr (D == 128) {
-            const uint2 v = lds64(at);
+            const uint2 v = smem_at<uint2>(at);
             w[r][0] = v.x;
             w[r][1] = v.y;
           } else {
-            w[r][0] = lds32(at);
+            w[r][0] = smem_at<uint32_t>(at);
           }
         }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t af[4];
-          int4_pair(w[0][k / 2] >> (8 * (k & 1)), af[0], af[2]);
-          int4_pair(w[1][k / 2] >> (8 * (k & 1)), af[1], af[3]);
+          int4_pair(mg, w[0][k / 2] >> (8 * (k & 1)), af[0], af[2]);
+          int4_pair(mg, w[1][k / 2] >> (8 * (k & 1)), af[1], af[3]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
+          for (int nb = 0; nb < NB; ++nb) {
+            if (k == 0)
+              mma_f16_16816_zero(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
+            else
+              mma_f16_16816(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
+          }
         }
       }
 #pragma unroll
@@ -640,35 +670,38 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
         }
       }
       // Slots 2 t4, 2 t4 + 1 and 8 more: this lane's tokens in V.
-      const uint32_t v0 = 16 * bb + int4_slot_row<D>(2 * t4), v1 = 16 * bb + int4_slot_row<D>(2 * t4 + 1);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t x[2][2];          // [slots 0-7, 8-15][low, high half of the words]: two tokens' halves
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint32_t a0 = int4_code_addr<D>(st + L::kV, v0 + 8 * r, h * (D / 4) + g * (D / 32));
-          const uint32_t a1 = int4_code_addr<D>(st + L::kV, v1 + 8 * r, h * (D / 4) + g * (D / 32));
+          const uint8_t* a0 = st + v_at[h][0] + (2 * bb + r) * kEight;
+          const uint8_t* a1 = st + v_at[h][1] + (2 * bb + r) * kEight;
           if constexpr (D == 128) {
-            const uint32_t w0 = lds32(a0), w1 = lds32(a1);
+            const uint32_t w0 = smem_at<uint32_t>(a0), w1 = smem_at<uint32_t>(a1);
             x[r][0] = __byte_perm(w0, w1, 0x5410);
             x[r][1] = __byte_perm(w0, w1, 0x7632);
           } else {
-            x[r][0] = __byte_perm(lds16(a0), lds16(a1), 0x5410);
+            x[r][0] = __byte_perm(smem_at<uint16_t>(a0), smem_at<uint16_t>(a1), 0x5410);
             x[r][1] = 0u;
           }
         }
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           uint32_t vf[4];
-          int4_pair(x[0][j / 2] >> (8 * (j & 1)), vf[0], vf[1]);
-          int4_pair(x[1][j / 2] >> (8 * (j & 1)), vf[2], vf[3]);
+          int4_pair(mg, x[0][j / 2] >> (8 * (j & 1)), vf[0], vf[1]);
+          int4_pair(mg, x[1][j / 2] >> (8 * (j & 1)), vf[2], vf[3]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma_f16_16816(acc[nb][h][j], vf, pb[nb][h][0], pb[nb][h][1]);
         }
       }
     }
-    __syncwarp();
-    if (issued < mine) issue(issued++);
+    __syncwarp();                                      // the stage is read: refill it
+    if (issued < mine) issue(issued++, stage);
+    if (++stage == kInt4Stages) {
+      stage = 0;
+      phase ^= 1;
+    }
   }
   grid_dependents_launch();
   if (failed && lane == 0) {

@@ -206,16 +206,6 @@ __device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* tm, int he
                : "memory");
 }
 
-// D = A B with a zero accumulator (m16n8k16, f16 inputs, fp32 result).
-__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t (&a)[4],
-                                                   uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 template <class T>
 __device__ __forceinline__ T smem_at(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
@@ -242,15 +232,18 @@ struct Int4DecodeArgs {
   int prefetch_units;     // units per warp pulled into L2 before the wait on the previous grid
 };
 
-// Nibbles 0, 1 (bits 0-3 and 4-7) of each half of x as f16 pairs c - 8.  The
-// subtraction is exact, and products with c - 8 instead of 1024 + c keep the
-// fp32 sums small.
+// Nibbles 0, 1 (bits 0-3 and 4-7) of each half of x as f16 pairs: c - 8 and,
+// for CENTRED, c - 8 again, otherwise 64 + c.  The subtractions are exact.
+template <bool CENTRED>
 __device__ __forceinline__ void int4_pair(const Int4Magic& mg, uint32_t x, uint32_t& n0, uint32_t& n1) {
-  const uint32_t lo = and_or(x, 0x000f000fu, mg.k1024), hi = and_or(x, 0x00f000f0u, mg.k64);
+  const uint32_t lo = and_or(x, 0x000f000fu, mg.k1024);
   const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), __half2half2(__ushort_as_half(0x6408)));
-  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), __half2half2(__ushort_as_half(0x5480)));
   n0 = *reinterpret_cast<const uint32_t*>(&a);
-  n1 = *reinterpret_cast<const uint32_t*>(&b);
+  n1 = and_or(x, 0x00f000f0u, mg.k64);
+  if constexpr (CENTRED) {
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&n1), __half2half2(__ushort_as_half(0x5480)));
+    n1 = *reinterpret_cast<const uint32_t*>(&b);
+  }
 }
 
 template <int D, int NB>
@@ -412,8 +405,11 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 
   // ---- q: f16 relative to the head's largest entry, in the order of K's
   // codes: word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
+  // The 64 + c pairs of K enter the products as they are: the sums start at
+  // -72 sum(q) over their channels (odd nibbles), which leaves c - 8.
   uint32_t qf[NB][2][KS][2];
-  float sq[NB][2][2], scl[NB][2];      // per column 2 t4 + c: sum of q per group, scale
+  float sq[NB][2][2], s0[NB][2][2], scl[NB][2];   // per column 2 t4 + c: sum of q per group,
+                                                  // where the scores start, scale
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const bool live = nb * 8 + g < a.G;
@@ -425,48 +421,56 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
       for (int w = 0; w < KS / 2; ++w) {
         raw[h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
+        if (!live) raw[h][w] = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
       }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    int e = 0;
-    if (live && mx <= 3.4e38f) frexpf(mx, &e);        // mx = f 2^e, f in [0.5, 1); 0 for 0
-    float sum[2] = {0.f, 0.f};
+    // 2^e with mx 2^-e in [1, 2), e in [-126, 126] (smaller rows stay below 1);
+    // an infinity keeps e = 126 and stays one.
+    const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    float sum[2], odd[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      sum[h] = odd[h] = 0.f;
 #pragma unroll
       for (int w = 0; w < KS / 2; ++w) {
         const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
-        __half y[8];
+        float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float f = live ? ldexpf((i & 1) ? bf16_hi(x[i / 2]) : bf16_lo(x[i / 2]), -e) : 0.f;
-          y[i] = __float2half_rn(f);
-          sum[h] += __half2float(y[i]);
+          y[i] = ((i & 1) ? bf16_hi(x[i / 2]) : bf16_lo(x[i / 2])) * down;
+          if (i & 1)
+            odd[h] += y[i];
+          else
+            sum[h] += y[i];
         }
         // k-step 2w + s: slots 2t, 2t+1 are nibbles 2s, 2s+4, slots 2t+8, 2t+9
         // nibbles 2s+1, 2s+5 (the pairs that one mask leaves).
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const __half2 v = __halves2half2(y[2 * s + i], y[2 * s + i + 4]);
-            qf[nb][h][2 * w + s][i] = *reinterpret_cast<const uint32_t*>(&v);
-          }
+          for (int i = 0; i < 2; ++i) qf[nb][h][2 * w + s][i] = pack_f16x2(y[2 * s + i], y[2 * s + i + 4]);
       }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
-      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+      for (int off = 1; off < 4; off <<= 1) {
+        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], off);
+        odd[h] += __shfl_xor_sync(0xffffffffu, odd[h], off);
+      }
     }
-    const float sc = ldexpf(a.scale_log2, e);
+    const float sc = a.scale_log2 * up;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int from = 8 * t4 + 4 * c;                // a lane of head 2 t4 + c
-      sq[nb][0][c] = __shfl_sync(0xffffffffu, sum[0], from);
-      sq[nb][1][c] = __shfl_sync(0xffffffffu, sum[1], from);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sq[nb][h][c] = __shfl_sync(0xffffffffu, sum[h] + odd[h], from);
+        s0[nb][h][c] = __shfl_sync(0xffffffffu, -72.f * odd[h], from);
+      }
       scl[nb][c] = __shfl_sync(0xffffffffu, sc, from);
     }
   }
@@ -536,6 +540,12 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     for (int bb = 0; bb < 2; ++bb) {
       float sc[NB][2][4];
 #pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[nb][h][x] = s0[nb][h][x & 1];
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[2][KS / 2];
 #pragma unroll
@@ -552,15 +562,10 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t af[4];
-          int4_pair(mg, w[0][k / 2] >> (8 * (k & 1)), af[0], af[2]);
-          int4_pair(mg, w[1][k / 2] >> (8 * (k & 1)), af[1], af[3]);
+          int4_pair<false>(mg, w[0][k / 2] >> (8 * (k & 1)), af[0], af[2]);
+          int4_pair<false>(mg, w[1][k / 2] >> (8 * (k & 1)), af[1], af[3]);
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if (k == 0)
-              mma_f16_16816_zero(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
-            else
-              mma_f16_16816(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
-          }
+          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
         }
       }
 #pragma unroll
@@ -614,10 +619,10 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
         for (int off = 1; off < 32; off <<= 1) vtop[h] = fmaxf(vtop[h], __shfl_xor_sync(0xffffffffu, vtop[h], off));
         keep_r[h] = 1.f;
         if (vtop[h] * inv_r[h] > 1.f) {
-          int e;
-          frexpf(vtop[h], &e);                        // vtop < 2^e, e <= 126 as vs < 2^126
-          const float r = ldexpf(1.f, -max(e, -126));
-          keep_r[h] = r / inv_r[h];                   // old R / new R; 0 from the initial 2^-126
+          // R is the power of two above vtop (scales are below 2^126).
+          const uint32_t e = min((__float_as_uint(vtop[h]) >> 23) + 1u, 253u);
+          const float r = __uint_as_float((254u - e) << 23);
+          keep_r[h] = r / inv_r[h];                   // old R / new R
           inv_r[h] = r;
         }
       }
@@ -689,8 +694,8 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
           uint32_t vf[4];
-          int4_pair(mg, x[0][j / 2] >> (8 * (j & 1)), vf[0], vf[1]);
-          int4_pair(mg, x[1][j / 2] >> (8 * (j & 1)), vf[2], vf[3]);
+          int4_pair<true>(mg, x[0][j / 2] >> (8 * (j & 1)), vf[0], vf[1]);
+          int4_pair<true>(mg, x[1][j / 2] >> (8 * (j & 1)), vf[2], vf[3]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma_f16_16816(acc[nb][h][j], vf, pb[nb][h][0], pb[nb][h][1]);
         }

@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(256) fd_expand_int4_kernel(const ExpandArgs a)
 constexpr int kUnit = 32;
 constexpr int kInt4Warps = 8;
 constexpr int kInt4Stages = 3;
-constexpr float kRescaleLog2 = 8.f;   // softmax weights up to 2^8 before a rescale
+constexpr float kRescaleLog2 = 8.f;   // a score may pass the reference by 2^8 ...
+constexpr float kWeightLog2 = 7.f;    // ... whose own weight is 2^7
 
 // 4-D tile load and L2 prefetch: {byte, head, row, plane}.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, uint32_t bar,
@@ -211,39 +212,19 @@ __device__ __forceinline__ T smem_at(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
 }
 
-// (x & mask) | bits in one instruction.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
-  return y;
-}
-
-// Exponents that turn a nibble into an f16 number: 1024 + c with the nibble in
-// the low mantissa bits, 64 + c with it four bits higher.  They come in as
-// kernel arguments: as constants the compiler spends a second instruction per
-// pair on them (one logic operation takes one immediate).
-struct Int4Magic {
-  uint32_t k1024, k64;       // 0x64006400, 0x54005400
-};
-
 struct Int4DecodeArgs {
   SplitArgs a;            // as fd_split_kernel's; k_scale and v_scale do not apply
-  Int4Magic magic;
   int prefetch_units;     // units per warp pulled into L2 before the wait on the previous grid
 };
 
-// Nibbles 0, 1 (bits 0-3 and 4-7) of each half of x as f16 pairs: c - 8 and,
-// for CENTRED, c - 8 again, otherwise 64 + c.  The subtractions are exact.
-template <bool CENTRED>
-__device__ __forceinline__ void int4_pair(const Int4Magic& mg, uint32_t x, uint32_t& n0, uint32_t& n1) {
-  const uint32_t lo = and_or(x, 0x000f000fu, mg.k1024);
-  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), __half2half2(__ushort_as_half(0x6408)));
-  n0 = *reinterpret_cast<const uint32_t*>(&a);
-  n1 = and_or(x, 0x00f000f0u, mg.k64);
-  if constexpr (CENTRED) {
-    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&n1), __half2half2(__ushort_as_half(0x5480)));
-    n1 = *reinterpret_cast<const uint32_t*>(&b);
-  }
+// D = A B, m16n8k16, f16 inputs, fp32 result.
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t (&a)[4],
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 template <int D, int NB>
@@ -290,26 +271,35 @@ __device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
 // Split kernel of a 4-bit cache: one CTA per (split, KV head, sequence), as
 // fd_split_kernel, with the units of 32 tokens dealt to its warps in turn.
 //
-// Scores.  S^T = (c - 8) q^T on m16n8k16 MMAs (16 tokens by up to 8 heads), one
-// fp32 sum per group of channels; then, per token,
-//   t = ks0 S0 + ks1 S1 + kb0 sum_0(q) + kb1 sum_1(q),
-// so that no scale touches an entry.  q is held in f16 relative to its row's
-// largest entry (a power of two), which keeps the 8 bits of every bf16 entry
-// that is not 2^14 times smaller than the largest.
-// P V.  O^T += (c - 8)^T w on the same MMAs, w = f16(p vs / R) with R a power of
-// two at least as large as every vs the warp has seen (f16's 11 bits; p vs of
-// any size fits), and the biases' part sum_j p_j vb_j in fp32 beside it.
-// A nibble pair costs one logic operation and one subtraction.  V's pairs run
-// along the tokens, so two tokens' words are merged first.
+// No code is converted.  A nibble in the low four bits of a half word is the f16
+// subnormal c 2^-24 as it stands, one in the next four bits c 2^-20, both exact
+// on the tensor cores: masks and shifts unpack the codes, 5 operations per 8
+// codes of K and 6 of V (whose pairs run along the tokens, so that two tokens'
+// words are merged first).  The e4m3 reading of a nibble, c 2^-9, takes 3, but
+// mma.sync spends 6 conversions on each e4m3 instruction here (measured: 105 a
+// unit, and 38.0 us against 29.7 us at 64K tokens of the CodeLlama-34B heads).
+// Scores.  S^T = c q^T on m16n8k16 f16 MMAs (16 tokens by up to 8 heads), one
+// fp32 sum per group of channels.  q is scaled by a power of two that brings its
+// largest entry to [2^14, 2^15), for the channels in odd nibbles 2^4 less, which
+// keeps the 8 bits of every bf16 entry down to 2^-24 of the largest.  Then, per
+// token,
+//   t = ks0 S0 + ks1 S1 + (kb0 - 8 ks0) sum_0(q) + (kb1 - 8 ks1) sum_1(q),
+// so that no scale touches an entry.
+// P V.  O^T += c^T w on the same MMAs, w = f16(p vs / R) with R a power of
+// two above every vs the warp has seen (f16's 11 bits; p vs of any size fits).
+// One more MMA per group sums 8 w as the tensor core sees it, which the end
+// takes off: c - 8, with no rounding of w left in it.  The biases' part
+// sum_j p_j vb_j is summed in fp32 beside it.
 // The running maximum is only moved when a score passes it by 2^8 (a vote per
-// unit in place of shuffles): weights up to 2^8 until then.
+// unit in place of shuffles), and the weights are 2^7 p, so that they use f16's
+// range: up to 2^15, and down to 2^-31 of the largest before one is lost.
 template <int D, int NB>
 __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     fd_split_int4_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmP, const Int4DecodeArgs p) {
   using L = Int4Smem<D, NB>;
-  constexpr int KS = D / 32;          // k-steps of a group's score MMA
+  constexpr int KW = D / 64;          // words of K's codes a lane holds per row and group
   constexpr int MB = D / 32;          // m-blocks of a group's P V MMA
   const SplitArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
@@ -403,23 +393,21 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
   int issued = 0;
   for (; issued < min(mine, kInt4Stages); ++issued) issue(issued, issued);
 
-  // ---- q: f16 relative to the head's largest entry, in the order of K's
-  // codes: word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
-  // The 64 + c pairs of K enter the products as they are: the sums start at
-  // -72 sum(q) over their channels (odd nibbles), which leaves c - 8.
-  uint32_t qf[NB][2][KS][2];
-  float sq[NB][2][2], s0[NB][2][2], scl[NB][2];   // per column 2 t4 + c: sum of q per group,
-                                                  // where the scores start, scale
+  // ---- q in f16, in the order of K's codes: word w of lane t4 in group h
+  // holds channels h D/2 + t4 D/8 + 8 w ..; k-step s of the word takes nibbles
+  // 2s, 2s+4 (slots 2 t4, 2 t4 + 1) and 2s+1, 2s+5 (slots 2 t4 + 8, + 9).
+  uint32_t qf[NB][2][KW][2][2];
+  float sq[NB][2][2], scl[NB][2];      // per column 2 t4 + c: sum of q per group, scale
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const bool live = nb * 8 + g < a.G;
     const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(b) * a.Hq + h0 + (live ? nb * 8 + g : 0)) * D;
-    uint4 raw[2][KS / 2];
+    uint4 raw[2][KW];
     float mx = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int w = 0; w < KS / 2; ++w) {
+      for (int w = 0; w < KW; ++w) {
         raw[h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
         if (!live) raw[h][w] = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
@@ -428,73 +416,66 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
       }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // 2^e with mx 2^-e in [1, 2), e in [-126, 126] (smaller rows stay below 1);
-    // an infinity keeps e = 126 and stays one.
-    const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126), 126);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    float sum[2], odd[2];
+    // mx 2^-e in [1, 2) (rows below 2^-112 stay below 1).
+    const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -112), 127);
+    const float down = __uint_as_float(static_cast<uint32_t>(141 - e) << 23);    // 2^(14 - e)
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);      // 2^e
+    float sum[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      sum[h] = odd[h] = 0.f;
+      sum[h] = 0.f;
 #pragma unroll
-      for (int w = 0; w < KS / 2; ++w) {
+      for (int w = 0; w < KW; ++w) {
         const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           y[i] = ((i & 1) ? bf16_hi(x[i / 2]) : bf16_lo(x[i / 2])) * down;
-          if (i & 1)
-            odd[h] += y[i];
-          else
-            sum[h] += y[i];
+          sum[h] += y[i];
         }
-        // k-step 2w + s: slots 2t, 2t+1 are nibbles 2s, 2s+4, slots 2t+8, 2t+9
-        // nibbles 2s+1, 2s+5 (the pairs that one mask leaves).
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) qf[nb][h][2 * w + s][i] = pack_f16x2(y[2 * s + i], y[2 * s + i + 4]);
+        for (int s = 0; s < 2; ++s) {
+          qf[nb][h][w][s][0] = pack_f16x2(y[2 * s], y[2 * s + 4]);
+          qf[nb][h][w][s][1] = pack_f16x2(y[2 * s + 1] * 0.0625f, y[2 * s + 5] * 0.0625f);
+        }
       }
 #pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], off);
-        odd[h] += __shfl_xor_sync(0xffffffffu, odd[h], off);
-      }
+      for (int off = 1; off < 4; off <<= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], off);
     }
-    const float sc = a.scale_log2 * up;
+    // S holds q 2^(14 - e) (c 2^-24): the sums of q take the same factor, and
+    // the scale its inverse, 2^(e + 10).
+    const float sc = a.scale_log2 * up * 1024.f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int from = 8 * t4 + 4 * c;                // a lane of head 2 t4 + c
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sq[nb][h][c] = __shfl_sync(0xffffffffu, sum[h] + odd[h], from);
-        s0[nb][h][c] = __shfl_sync(0xffffffffu, -72.f * odd[h], from);
-      }
+      for (int h = 0; h < 2; ++h) sq[nb][h][c] = __shfl_sync(0xffffffffu, sum[h] * 0x1p-24f, from);
       scl[nb][c] = __shfl_sync(0xffffffffu, sc, from);
     }
   }
 
-  // ---- softmax state.  Per column: the reference m (in units of t), m scl as
-  // it enters the weights, and the t beyond which it moves.
-  float m_ref[NB][2], m_log2[NB][2], bound[NB][2], l_run[NB][2], bias[NB][2][2];
-  float acc[NB][2][MB][4];
+  // ---- softmax state.  Per column: the reference (log2 units; a weight is
+  // 2^(t scl - ref)) and the t beyond which it moves.
+  float ref[NB][2], bound[NB][2], l_run[NB][2], bias[NB][2][2];
+  float acc[NB][2][MB][4], eight[NB][4];              // c w; 8 w of group 0 and of group 1
   float inv_r[2] = {0x1p126f, 0x1p126f};              // 1 / R per group
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      m_ref[nb][c] = bound[nb][c] = -INFINITY;
-      m_log2[nb][c] = l_run[nb][c] = bias[nb][0][c] = bias[nb][1][c] = 0.f;
+      bound[nb][c] = -INFINITY;
+      ref[nb][c] = l_run[nb][c] = bias[nb][0][c] = bias[nb][1][c] = 0.f;
     }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int i = 0; i < 4; ++i) {
+      eight[nb][i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < MB; ++j)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nb][h][j][i] = 0.f;
+        for (int j = 0; j < MB; ++j) acc[nb][h][j][i] = 0.f;
+    }
 
   // Offsets within a unit of this lane's loads: codes of K (slot g), of V
   // (slots 2 t4 and 2 t4 + 1) and the record of slot g.
@@ -508,7 +489,6 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     v_at[h][1] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4 + 1), h * (D / 4) + g * (D / 32));
   }
   const uint32_t p_at = L::kP + k_row * 16;
-  const Int4Magic mg = p.magic;
   bool failed = false;
   uint32_t stage = 0, phase = 0;
   for (int i = 0; i < mine; ++i) {
@@ -540,14 +520,8 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     for (int bb = 0; bb < 2; ++bb) {
       float sc[NB][2][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[nb][h][x] = s0[nb][h][x & 1];
-#pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[2][KS / 2];
+        uint32_t w[2][KW];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint8_t* at = st + k_at[h] + (2 * bb + r) * kEight;
@@ -560,26 +534,34 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
           }
         }
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t af[4];
-          int4_pair<false>(mg, w[0][k / 2] >> (8 * (k & 1)), af[0], af[2]);
-          int4_pair<false>(mg, w[1][k / 2] >> (8 * (k & 1)), af[1], af[3]);
+        for (int k = 0; k < KW; ++k)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma_f16_16816(sc[nb][h], af, qf[nb][h][k][0], qf[nb][h][k][1]);
-        }
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t y0 = w[0][k] >> (8 * s), y1 = w[1][k] >> (8 * s);
+            const uint32_t af[4] = {y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              if (k == 0 && s == 0)
+                mma_f16_16816_zero(sc[nb][h], af, qf[nb][h][k][s][0], qf[nb][h][k][s][1]);
+              else
+                mma_f16_16816(sc[nb][h], af, qf[nb][h][k][s][0], qf[nb][h][k][s][1]);
+            }
+          }
       }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int r = 0; r < 2; ++r) {
+        const float ks0 = bf16_lo(rec[bb][r].x), ks1 = bf16_lo(rec[bb][r].y);
+        const float kb0 = fmaf(-8.f, ks0, bf16_hi(rec[bb][r].x)), kb1 = fmaf(-8.f, ks1, bf16_hi(rec[bb][r].y));
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = bf16_hi(rec[bb][r].x) * sq[nb][0][c];
-            x = fmaf(bf16_hi(rec[bb][r].y), sq[nb][1][c], x);
-            x = fmaf(bf16_lo(rec[bb][r].x), sc[nb][0][2 * r + c], x);
-            x = fmaf(bf16_lo(rec[bb][r].y), sc[nb][1][2 * r + c], x);
-            t[nb][bb][r][c] = x;
+            float x = kb0 * sq[nb][0][c];
+            x = fmaf(kb1, sq[nb][1][c], x);
+            x = fmaf(ks0, sc[nb][0][2 * r + c], x);
+            t[nb][bb][r][c] = fmaf(ks1, sc[nb][1][2 * r + c], x);
           }
+      }
     }
     if (valid < kUnit) {
 #pragma unroll
@@ -633,16 +615,18 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1)
             top[nb][c] = fmaxf(top[nb][c], __shfl_xor_sync(0xffffffffu, top[nb][c], off));
-          const float m = fmaxf(m_ref[nb][c], top[nb][c]);
-          const float ml = m == -INFINITY ? 0.f : m * scl[nb][c];
-          const float al = m_ref[nb][c] == -INFINITY ? 0.f : ex2(m_log2[nb][c] - ml);
-          m_ref[nb][c] = m;
-          m_log2[nb][c] = ml;
-          if (m != -INFINITY) bound[nb][c] = m + fminf(kRescaleLog2 / scl[nb][c], 3e38f);
+          float al = 1.f;
+          if (top[nb][c] > bound[nb][c]) {
+            const float now = fmaf(top[nb][c], scl[nb][c], -kWeightLog2);
+            al = bound[nb][c] == -INFINITY ? 0.f : ex2(ref[nb][c] - now);
+            ref[nb][c] = now;
+            bound[nb][c] = top[nb][c] + fminf(kRescaleLog2 / scl[nb][c], 3e38f);
+          }
           l_run[nb][c] *= al;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             bias[nb][h][c] *= al;
+            eight[nb][2 * h + c] *= al * keep_r[h];
 #pragma unroll
             for (int j = 0; j < MB; ++j) {
               acc[nb][h][j][c] *= al * keep_r[h];
@@ -665,7 +649,7 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
           float e[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], -m_log2[nb][c]));
+            e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], -ref[nb][c]));
             l_run[nb][c] += e[c];
             bias[nb][0][c] = fmaf(e[c], vb[0], bias[nb][0][c]);
             bias[nb][1][c] = fmaf(e[c], vb[1], bias[nb][1][c]);
@@ -691,14 +675,19 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
             x[r][1] = 0u;
           }
         }
+        // Nibbles 2j and 2j + 1 of the two tokens' halves, as f16 subnormals.
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          uint32_t vf[4];
-          int4_pair<true>(mg, x[0][j / 2] >> (8 * (j & 1)), vf[0], vf[1]);
-          int4_pair<true>(mg, x[1][j / 2] >> (8 * (j & 1)), vf[2], vf[3]);
+          const uint32_t y0 = x[0][j / 2] >> (8 * (j & 1)), y1 = x[1][j / 2] >> (8 * (j & 1));
+          const uint32_t vf[4] = {y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u};
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma_f16_16816(acc[nb][h][j], vf, pb[nb][h][0], pb[nb][h][1]);
         }
+        // The code 8 in 8 rows: sums of 8 w, group 0 in rows 0-7, group 1 in 8-15.
+        const uint32_t v8[4] = {h == 0 ? 0x00080008u : 0u, h == 1 ? 0x00080008u : 0u,
+                                h == 0 ? 0x00080008u : 0u, h == 1 ? 0x00080008u : 0u};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma_f16_16816(eight[nb], v8, pb[nb][h][0], pb[nb][h][1]);
       }
     }
     __syncwarp();                                      // the stage is read: refill it
@@ -734,15 +723,17 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
       const int col = nb * 8 + 2 * t4 + c;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float r = 1.f / inv_r[h];
+        const float r = 1.f / inv_r[h], r0 = r * 0x1p24f, r1 = r * 0x1p20f;
+        const float w8 = eight[nb][2 * h + c];
         float* o = f + col * L::kAccStride + h * (D / 2) + g * (D / 16);
 #pragma unroll
         for (int j = 0; j < MB; ++j)
           *reinterpret_cast<float2*>(o + 2 * j) =
-              make_float2(fmaf(acc[nb][h][j][c], r, bias[nb][h][c]), fmaf(acc[nb][h][j][c + 2], r, bias[nb][h][c]));
+              make_float2(fmaf(acc[nb][h][j][c] - w8, r0, bias[nb][h][c]),
+                          fmaf(acc[nb][h][j][c + 2] - 16.f * w8, r1, bias[nb][h][c]));
       }
       if (g == 0) {
-        f[L::kM + col] = m_ref[nb][c] == -INFINITY && l_run[nb][c] == 0.f ? -INFINITY : m_log2[nb][c];
+        f[L::kM + col] = bound[nb][c] == -INFINITY && l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
         f[L::kL + col] = l_run[nb][c];
       }
     }

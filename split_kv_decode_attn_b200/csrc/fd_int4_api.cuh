@@ -268,7 +268,6 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.tile_r = chunks.tiles % chunks.splits;
   a.scale_log2 = scale * 1.4426950408889634074f;
   a.scale = scale;
-  d.magic = fd::Int4Magic{0x64006400u, 0x54005400u};
   d.prefetch_units = p->block_size ? 0 : fd::kInt4Stages;
   const dim3 grid(static_cast<unsigned>(chunks.splits), static_cast<unsigned>(p->Hkv),
                   static_cast<unsigned>(p->B));

@@ -180,11 +180,14 @@ __global__ void __launch_bounds__(256) fd_expand_int4_kernel(const ExpandArgs a)
 
 // ---------------------------------------------------------------- decode
 
-// A warp streams units of 32 tokens through a ring of its own: it issues its
+// A warp streams units of tokens through a ring of its own: it issues its
 // copies, waits for them and computes, with no other warp to wait for.
-constexpr int kUnit = 32;
-constexpr int kInt4Warps = 8;
-constexpr int kInt4Stages = 3;
+//   WARPS   warps per CTA        CTAS    CTAs per SM the registers allow
+//   UNIT    tokens per unit      STAGES  units per ring
+template <int WARPS_, int CTAS_, int UNIT_, int STAGES_>
+struct Int4Shape {
+  static constexpr int WARPS = WARPS_, CTAS = CTAS_, UNIT = UNIT_, STAGES = STAGES_;
+};
 constexpr float kRescaleLog2 = 8.f;   // a score may pass the reference by 2^8 ...
 constexpr float kWeightLog2 = 7.f;    // ... whose own weight is 2^7
 
@@ -227,14 +230,16 @@ __device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-template <int D, int NB>
+template <int D, int NB, class SH>
 struct Int4Smem {
+  static constexpr int kUnit = SH::UNIT, kInt4Warps = SH::WARPS, kInt4Stages = SH::STAGES;
   static constexpr int kRowBytes = D / 2;
   static constexpr int kCodeBytes = kUnit * kRowBytes;
   static constexpr int kV = kCodeBytes;                 // offsets within a stage
   static constexpr int kP = 2 * kCodeBytes;
   static constexpr int kStageBytes = 2 * kCodeBytes + kUnit * 16;
-  static constexpr int kWarpBytes = kInt4Stages * kStageBytes;
+  static constexpr int kDecoded = kInt4Stages * kStageBytes;   // records of a unit in fp32, K's then V's
+  static constexpr int kWarpBytes = (kDecoded + kUnit * 32 + 511) / 512 * 512;
   static constexpr int kBarOffset = kInt4Warps * kWarpBytes;
   static constexpr int kErrorOffset = kBarOffset + 8 * kInt4Warps * kInt4Stages;
   static constexpr int kDynamicBytes = kErrorOffset + 16 + 1024;   // room to align to 1 KB
@@ -293,12 +298,14 @@ __device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
 // The running maximum is only moved when a score passes it by 2^8 (a vote per
 // unit in place of shuffles), and the weights are 2^7 p, so that they use f16's
 // range: up to 2^15, and down to 2^-31 of the largest before one is lost.
-template <int D, int NB>
-__global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
+template <int D, int NB, class SH>
+__global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     fd_split_int4_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmP, const Int4DecodeArgs p) {
-  using L = Int4Smem<D, NB>;
+  using L = Int4Smem<D, NB, SH>;
+  constexpr int kUnit = SH::UNIT, kInt4Warps = SH::WARPS, kInt4Stages = SH::STAGES;
+  constexpr int BB = kUnit / 16;      // 16-token blocks per unit
   constexpr int KW = D / 64;          // words of K's codes a lane holds per row and group
   constexpr int MB = D / 32;          // m-blocks of a group's P V MMA
   const SplitArgs& a = p.a;
@@ -335,9 +342,24 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
   __syncthreads();
   grid_dependency_wait();
 
+  // q's loads go ahead of the copies (behind them they took 2 us more to come
+  // back): word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
+  const int h0 = kvh * a.G;
+  uint4 raw[NB][2][KW];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const bool live = nb * 8 + g < a.G;
+    const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(b) * a.Hq + h0 + (live ? nb * 8 + g : 0)) * D;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        raw[nb][h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
+        if (!live) raw[nb][h][w] = make_uint4(0u, 0u, 0u, 0u);
+      }
+  }
   const int n = seq_length(a.seqlens, b, a.max_len);
   const int end = min(split_end, n);
-  const int h0 = kvh * a.G;
   const int n_parts = (a.n_splits == 1 || (n + kTile - 1) / kTile <= a.tile_q) ? 1 : 2;
   if (start >= end) {
     if (split == 0) {   // an empty sequence
@@ -393,24 +415,18 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
   int issued = 0;
   for (; issued < min(mine, kInt4Stages); ++issued) issue(issued, issued);
 
-  // ---- q in f16, in the order of K's codes: word w of lane t4 in group h
-  // holds channels h D/2 + t4 D/8 + 8 w ..; k-step s of the word takes nibbles
+  // ---- q in f16, in the order of K's codes: k-step s of a word takes nibbles
   // 2s, 2s+4 (slots 2 t4, 2 t4 + 1) and 2s+1, 2s+5 (slots 2 t4 + 8, + 9).
   uint32_t qf[NB][2][KW][2][2];
   float sq[NB][2][2], scl[NB][2];      // per column 2 t4 + c: sum of q per group, scale
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const bool live = nb * 8 + g < a.G;
-    const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(b) * a.Hq + h0 + (live ? nb * 8 + g : 0)) * D;
-    uint4 raw[2][KW];
     float mx = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        raw[h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
-        if (!live) raw[h][w] = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
+        const uint32_t x[4] = {raw[nb][h][w].x, raw[nb][h][w].y, raw[nb][h][w].z, raw[nb][h][w].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(x[i])), fabsf(bf16_hi(x[i]))));
       }
@@ -426,7 +442,7 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
       sum[h] = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const uint32_t x[4] = {raw[h][w].x, raw[h][w].y, raw[h][w].z, raw[h][w].w};
+        const uint32_t x[4] = {raw[nb][h][w].x, raw[nb][h][w].y, raw[nb][h][w].z, raw[nb][h][w].w};
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -488,7 +504,8 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     v_at[h][0] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4), h * (D / 4) + g * (D / 32));
     v_at[h][1] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4 + 1), h * (D / 4) + g * (D / 32));
   }
-  const uint32_t p_at = L::kP + k_row * 16;
+  const uint8_t* k_rec = ring + L::kDecoded + k_row * 16;
+  const uint8_t* v_rec = k_rec + kUnit * 16;
   bool failed = false;
   uint32_t stage = 0, phase = 0;
   for (int i = 0; i < mine; ++i) {
@@ -500,24 +517,58 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
     }
     const int valid = end - unit_token(i);             // tokens of the unit that count
 
-    // Records of this lane's four tokens: block bb, slots g and g + 8.
-    uint4 rec[2][2];
+    // Records in fp32, one token per lane and 32 tokens: K's as ks0, kb0 - 8 ks0,
+    // ks1, kb1 - 8 ks1, V's as vs0 / R, vb0, vs1 / R, vb1; zeros for a token
+    // that does not count (its record and codes may be anything).  Read by the
+    // four lanes of a token afterwards: unpacking there took 29 more
+    // instructions per 32 tokens.
+    {
+      uint4 rec[kUnit / 32];
+      float vtop[2] = {0.f, 0.f};
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb)
+      for (int x = 0; x < kUnit / 32; ++x) {
+        rec[x] = smem_at<uint4>(st + L::kP + (32 * x + lane) * 16);
+        if (32 * x + lane >= valid) rec[x] = make_uint4(0u, 0u, 0u, 0u);
+        vtop[0] = fmaxf(vtop[0], fabsf(bf16_lo(rec[x].z)));
+        vtop[1] = fmaxf(vtop[1], fabsf(bf16_lo(rec[x].w)));
+      }
+      if (__any_sync(0xffffffffu, vtop[0] * inv_r[0] > 1.f || vtop[1] * inv_r[1] > 1.f)) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) rec[bb][r] = smem_at<uint4>(st + p_at + (16 * bb + 8 * r) * 16);
-    if (valid < kUnit) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int bb = 0; bb < 2; ++bb)
+          for (int off = 1; off < 32; off <<= 1) vtop[h] = fmaxf(vtop[h], __shfl_xor_sync(0xffffffffu, vtop[h], off));
+          if (vtop[h] * inv_r[h] > 1.f) {
+            // R becomes the power of two above vtop (scales are below 2^126).
+            const uint32_t e = min((__float_as_uint(vtop[h]) >> 23) + 1u, 253u);
+            const float r = __uint_as_float((254u - e) << 23), keep = r / inv_r[h];   // old R / new R
+            inv_r[h] = r;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (16 * bb + 8 * r + static_cast<int>(k_row) >= valid) rec[bb][r] = make_uint4(0u, 0u, 0u, 0u);
+            for (int nb = 0; nb < NB; ++nb) {
+              eight[nb][2 * h] *= keep;
+              eight[nb][2 * h + 1] *= keep;
+#pragma unroll
+              for (int j = 0; j < MB; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[nb][h][j][x] *= keep;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kUnit / 32; ++x) {
+        const float ks0 = bf16_lo(rec[x].x), ks1 = bf16_lo(rec[x].y);
+        float4* to = reinterpret_cast<float4*>(ring + L::kDecoded) + 32 * x + lane;
+        to[0] = make_float4(ks0, fmaf(-8.f, ks0, bf16_hi(rec[x].x)), ks1, fmaf(-8.f, ks1, bf16_hi(rec[x].y)));
+        to[kUnit] = make_float4(bf16_lo(rec[x].z) * inv_r[0], bf16_hi(rec[x].z), bf16_lo(rec[x].w) * inv_r[1],
+                                bf16_hi(rec[x].w));
+      }
+      __syncwarp();
     }
 
-    // Scores, t[bb][row][column].
-    float t[NB][2][2][2];
+    // Scores, t[..][row][column].
+    float t[NB][BB][2][2];
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb) {
+    for (int bb = 0; bb < BB; ++bb) {
       float sc[NB][2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -550,22 +601,21 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float ks0 = bf16_lo(rec[bb][r].x), ks1 = bf16_lo(rec[bb][r].y);
-        const float kb0 = fmaf(-8.f, ks0, bf16_hi(rec[bb][r].x)), kb1 = fmaf(-8.f, ks1, bf16_hi(rec[bb][r].y));
+        const float4 rec = smem_at<float4>(k_rec + (16 * bb + 8 * r) * 16);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = kb0 * sq[nb][0][c];
-            x = fmaf(kb1, sq[nb][1][c], x);
-            x = fmaf(ks0, sc[nb][0][2 * r + c], x);
-            t[nb][bb][r][c] = fmaf(ks1, sc[nb][1][2 * r + c], x);
+            float x = rec.y * sq[nb][0][c];
+            x = fmaf(rec.w, sq[nb][1][c], x);
+            x = fmaf(rec.x, sc[nb][0][2 * r + c], x);
+            t[nb][bb][r][c] = fmaf(rec.z, sc[nb][1][2 * r + c], x);
           }
       }
     }
     if (valid < kUnit) {
 #pragma unroll
-      for (int bb = 0; bb < 2; ++bb)
+      for (int bb = 0; bb < BB; ++bb)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
           if (16 * bb + 8 * r + static_cast<int>(k_row) >= valid) {
@@ -574,40 +624,19 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
           }
     }
 
-    // Does a score pass its bound, or a V scale R?
-    float top[NB][2], vtop[2];
+    // Does a score pass its bound?
+    float top[NB][2];
     bool move = false;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        top[nb][c] = fmaxf(fmaxf(t[nb][0][0][c], t[nb][0][1][c]), fmaxf(t[nb][1][0][c], t[nb][1][1][c]));
+        top[nb][c] = -INFINITY;
+#pragma unroll
+        for (int bb = 0; bb < BB; ++bb) top[nb][c] = fmaxf(top[nb][c], fmaxf(t[nb][bb][0][c], t[nb][bb][1][c]));
         move |= top[nb][c] > bound[nb][c];
       }
-    vtop[0] = vtop[1] = 0.f;
-#pragma unroll
-    for (int bb = 0; bb < 2; ++bb)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        vtop[0] = fmaxf(vtop[0], fabsf(bf16_lo(rec[bb][r].z)));
-        vtop[1] = fmaxf(vtop[1], fabsf(bf16_lo(rec[bb][r].w)));
-      }
-    move |= vtop[0] * inv_r[0] > 1.f || vtop[1] * inv_r[1] > 1.f;
     if (__any_sync(0xffffffffu, move)) {
-      float keep_r[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) vtop[h] = fmaxf(vtop[h], __shfl_xor_sync(0xffffffffu, vtop[h], off));
-        keep_r[h] = 1.f;
-        if (vtop[h] * inv_r[h] > 1.f) {
-          // R is the power of two above vtop (scales are below 2^126).
-          const uint32_t e = min((__float_as_uint(vtop[h]) >> 23) + 1u, 253u);
-          const float r = __uint_as_float((254u - e) << 23);
-          keep_r[h] = r / inv_r[h];                   // old R / new R
-          inv_r[h] = r;
-        }
-      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -615,22 +644,21 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1)
             top[nb][c] = fmaxf(top[nb][c], __shfl_xor_sync(0xffffffffu, top[nb][c], off));
-          float al = 1.f;
           if (top[nb][c] > bound[nb][c]) {
             const float now = fmaf(top[nb][c], scl[nb][c], -kWeightLog2);
-            al = bound[nb][c] == -INFINITY ? 0.f : ex2(ref[nb][c] - now);
+            const float al = bound[nb][c] == -INFINITY ? 0.f : ex2(ref[nb][c] - now);
             ref[nb][c] = now;
             bound[nb][c] = top[nb][c] + fminf(kRescaleLog2 / scl[nb][c], 3e38f);
-          }
-          l_run[nb][c] *= al;
+            l_run[nb][c] *= al;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            bias[nb][h][c] *= al;
-            eight[nb][2 * h + c] *= al * keep_r[h];
+            for (int h = 0; h < 2; ++h) {
+              bias[nb][h][c] *= al;
+              eight[nb][2 * h + c] *= al;
 #pragma unroll
-            for (int j = 0; j < MB; ++j) {
-              acc[nb][h][j][c] *= al * keep_r[h];
-              acc[nb][h][j][c + 2] *= al * keep_r[h];
+              for (int j = 0; j < MB; ++j) {
+                acc[nb][h][j][c] *= al;
+                acc[nb][h][j][c + 2] *= al;
+              }
             }
           }
         }
@@ -638,12 +666,11 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
 
     // Weights, and P V for the 16 tokens of each block.
 #pragma unroll
-    for (int bb = 0; bb < 2; ++bb) {
+    for (int bb = 0; bb < BB; ++bb) {
       uint32_t pb[NB][2][2];       // [group][slots 0-7, 8-15]
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float vs[2] = {bf16_lo(rec[bb][r].z) * inv_r[0], bf16_lo(rec[bb][r].w) * inv_r[1]};
-        const float vb[2] = {bf16_hi(rec[bb][r].z), bf16_hi(rec[bb][r].w)};
+        const float4 rec = smem_at<float4>(v_rec + (16 * bb + 8 * r) * 16);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float e[2];
@@ -651,11 +678,11 @@ __global__ void __launch_bounds__(kInt4Warps * 32, NB == 1 ? 2 : 1)
           for (int c = 0; c < 2; ++c) {
             e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], -ref[nb][c]));
             l_run[nb][c] += e[c];
-            bias[nb][0][c] = fmaf(e[c], vb[0], bias[nb][0][c]);
-            bias[nb][1][c] = fmaf(e[c], vb[1], bias[nb][1][c]);
+            bias[nb][0][c] = fmaf(e[c], rec.y, bias[nb][0][c]);
+            bias[nb][1][c] = fmaf(e[c], rec.w, bias[nb][1][c]);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) pb[nb][h][r] = movmatrix_trans(pack_f16x2(e[0] * vs[h], e[1] * vs[h]));
+          pb[nb][0][r] = movmatrix_trans(pack_f16x2(e[0] * rec.x, e[1] * rec.x));
+          pb[nb][1][r] = movmatrix_trans(pack_f16x2(e[0] * rec.z, e[1] * rec.z));
         }
       }
       // Slots 2 t4, 2 t4 + 1 and 8 more: this lane's tokens in V.

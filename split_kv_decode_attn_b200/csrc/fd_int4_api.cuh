@@ -106,11 +106,11 @@ fd_status cached_int4_maps(Int4Maps* m, const fd::Int4Cache& c, int D, int box_r
   return FD_OK;
 }
 
-template <int D, int NB>
+template <int D, int NB, class SH>
 fd_status launch_split_int4(const Int4Maps& m, const fd::Int4DecodeArgs& a, dim3 grid, int dev,
                             fd_stream_t s) {
-  using L = fd::Int4Smem<D, NB>;
-  auto kern = fd::fd_split_int4_kernel<D, NB>;
+  using L = fd::Int4Smem<D, NB, SH>;
+  auto kern = fd::fd_split_int4_kernel<D, NB, SH>;
   static std::atomic<unsigned long long> attr_ctx[kMaxDevices];   // as launch_split's
   const unsigned long long ctx = current_context_id();
   if (ctx == 0 || attr_ctx[dev].load() != ctx) {
@@ -119,7 +119,7 @@ fd_status launch_split_int4(const Int4Maps& m, const fd::Int4DecodeArgs& a, dim3
       return FD_ERR_CUDA;
     attr_ctx[dev].store(ctx);
   }
-  return launch_chained(kern, grid, fd::kInt4Warps * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
+  return launch_chained(kern, grid, SH::WARPS * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
 }
 
 // Do two arrays of int32 share memory?
@@ -248,7 +248,10 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   const fd_status arch = this_device(&dev);
   if (arch != FD_OK) return arch;
   Int4Maps maps;
-  const int box_rows = p->block_size ? std::min(p->block_size, fd::kUnit) : fd::kUnit;
+  using ShapeN = fd::Int4Shape<8, 1, 64, 2>;
+  using ShapeW = fd::Int4Shape<8, 1, 32, 3>;
+  const int unit = p->Hq / p->Hkv <= 8 ? ShapeN::UNIT : ShapeW::UNIT;
+  const int box_rows = p->block_size ? std::min(p->block_size, unit) : unit;
   if (cached_int4_maps(&maps, c, p->D, box_rows, dev) != FD_OK) return FD_ERR_CUDA;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.seqlens = seqlens;
@@ -268,17 +271,17 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.tile_r = chunks.tiles % chunks.splits;
   a.scale_log2 = scale * 1.4426950408889634074f;
   a.scale = scale;
-  d.prefetch_units = p->block_size ? 0 : fd::kInt4Stages;
+  d.prefetch_units = p->block_size ? 0 : 3;
   const dim3 grid(static_cast<unsigned>(chunks.splits), static_cast<unsigned>(p->Hkv),
                   static_cast<unsigned>(p->B));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   fd_status r;
   if (p->D == 128)
-    r = a.G <= 8 ? launch_split_int4<128, 1>(maps, d, grid, dev, stream)
-                 : launch_split_int4<128, 2>(maps, d, grid, dev, stream);
+    r = a.G <= 8 ? launch_split_int4<128, 1, ShapeN>(maps, d, grid, dev, stream)
+                 : launch_split_int4<128, 2, ShapeW>(maps, d, grid, dev, stream);
   else
-    r = a.G <= 8 ? launch_split_int4<64, 1>(maps, d, grid, dev, stream)
-                 : launch_split_int4<64, 2>(maps, d, grid, dev, stream);
+    r = a.G <= 8 ? launch_split_int4<64, 1, ShapeN>(maps, d, grid, dev, stream)
+                 : launch_split_int4<64, 2, ShapeW>(maps, d, grid, dev, stream);
   if (r == FD_OK && chunks.splits > 1)
     r = p->D == 128 ? launch_combine<128>(a, p->B, s) : launch_combine<64>(a, p->B, s);
   return r;

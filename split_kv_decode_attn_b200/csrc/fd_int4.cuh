@@ -210,6 +210,13 @@ __device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* tm, int he
                : "memory");
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 template <class T>
 __device__ __forceinline__ T smem_at(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
@@ -238,9 +245,12 @@ struct Int4Smem {
   static constexpr int kV = kCodeBytes;                 // offsets within a stage
   static constexpr int kP = 2 * kCodeBytes;
   static constexpr int kStageBytes = 2 * kCodeBytes + kUnit * 16;
-  static constexpr int kDecoded = kInt4Stages * kStageBytes;   // records of a unit in fp32, K's then V's
-  static constexpr int kWarpBytes = (kDecoded + kUnit * 32 + 511) / 512 * 512;
-  static constexpr int kBarOffset = kInt4Warps * kWarpBytes;
+  static constexpr int kWarpBytes = kInt4Stages * kStageBytes;
+  // V's part of a unit's records, unpacked: vs0 / R, vs1 / R in fp32 per token,
+  // then vb0, vb1 in bf16.  (K's part, in fp32, takes the records' place.)
+  static constexpr int kVRecOffset = kInt4Warps * kWarpBytes;
+  static constexpr int kVRecBytes = kUnit * 12;
+  static constexpr int kBarOffset = kVRecOffset + kInt4Warps * kVRecBytes;
   static constexpr int kErrorOffset = kBarOffset + 8 * kInt4Warps * kInt4Stages;
   static constexpr int kDynamicBytes = kErrorOffset + 16 + 1024;   // room to align to 1 KB
   // A warp leaves its softmax state in its own drained ring (floats).
@@ -313,7 +323,9 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The warp's number from a shuffle: the compiler then keeps what follows from
+  // it, the addresses of copies and barriers, in uniform registers.
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   uint8_t* ring = smem + warp * L::kWarpBytes;
   const uint32_t ring_at = smem_u32(ring);
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     const uint32_t st = ring_at + s * L::kStageBytes;
     const uint32_t full = bar + 8 * s;
     if (!paged) {
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(full, kUnit * (D + 16));
         tma_load_4d(st, &tmK, full, kvh, t0, b, policy);
         tma_load_4d(st + L::kV, &tmV, full, kvh, t0, b, policy);
@@ -504,12 +516,14 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     v_at[h][0] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4), h * (D / 4) + g * (D / 32));
     v_at[h][1] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4 + 1), h * (D / 4) + g * (D / 32));
   }
-  const uint8_t* k_rec = ring + L::kDecoded + k_row * 16;
-  const uint8_t* v_rec = k_rec + kUnit * 16;
+  const uint32_t k_rec = L::kP + k_row * 16;           // within the unit
+  uint8_t* v_recs = smem + L::kVRecOffset + warp * L::kVRecBytes;
+  const uint8_t* vs_rec = v_recs + k_row * 8;
+  const uint8_t* vb_rec = v_recs + kUnit * 8 + k_row * 4;
   bool failed = false;
   uint32_t stage = 0, phase = 0;
   for (int i = 0; i < mine; ++i) {
-    const uint8_t* st = ring + stage * L::kStageBytes;
+    uint8_t* st = ring + stage * L::kStageBytes;
     const bool ok = mbar_wait(bar + 8 * stage, phase, kWaitLimitNs);
     if (!__all_sync(0xffffffffu, ok)) {
       failed = true;
@@ -517,10 +531,10 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     }
     const int valid = end - unit_token(i);             // tokens of the unit that count
 
-    // Records in fp32, one token per lane and 32 tokens: K's as ks0, kb0 - 8 ks0,
-    // ks1, kb1 - 8 ks1, V's as vs0 / R, vb0, vs1 / R, vb1; zeros for a token
-    // that does not count (its record and codes may be anything).  Read by the
-    // four lanes of a token afterwards: unpacking there took 29 more
+    // Records unpacked, one token per lane and 32 tokens: K's as ks0, kb0 - 8 ks0,
+    // ks1, kb1 - 8 ks1 in fp32 over the record, V's beside the ring; zeros for a
+    // token that does not count (its record and codes may be anything).  The four
+    // lanes of a token read them afterwards: unpacking there took 29 more
     // instructions per 32 tokens.
     {
       uint4 rec[kUnit / 32];
@@ -557,19 +571,21 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
 #pragma unroll
       for (int x = 0; x < kUnit / 32; ++x) {
         const float ks0 = bf16_lo(rec[x].x), ks1 = bf16_lo(rec[x].y);
-        float4* to = reinterpret_cast<float4*>(ring + L::kDecoded) + 32 * x + lane;
-        to[0] = make_float4(ks0, fmaf(-8.f, ks0, bf16_hi(rec[x].x)), ks1, fmaf(-8.f, ks1, bf16_hi(rec[x].y)));
-        to[kUnit] = make_float4(bf16_lo(rec[x].z) * inv_r[0], bf16_hi(rec[x].z), bf16_lo(rec[x].w) * inv_r[1],
-                                bf16_hi(rec[x].w));
+        const int at = 32 * x + lane;
+        *reinterpret_cast<float4*>(st + L::kP + at * 16) =
+            make_float4(ks0, fmaf(-8.f, ks0, bf16_hi(rec[x].x)), ks1, fmaf(-8.f, ks1, bf16_hi(rec[x].y)));
+        *reinterpret_cast<float2*>(v_recs + at * 8) =
+            make_float2(bf16_lo(rec[x].z) * inv_r[0], bf16_lo(rec[x].w) * inv_r[1]);
+        *reinterpret_cast<uint32_t*>(v_recs + kUnit * 8 + at * 4) = __byte_perm(rec[x].z, rec[x].w, 0x7632);
       }
       __syncwarp();
     }
 
     // Scores, t[..][row][column].
-    float t[NB][BB][2][2];
+    float t[NB][BB][2][2], scs[BB][NB][2][4];
 #pragma unroll
     for (int bb = 0; bb < BB; ++bb) {
-      float sc[NB][2][4];
+      auto& sc = scs[bb];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[2][KW];
@@ -599,9 +615,13 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
             }
           }
       }
+    }
+#pragma unroll
+    for (int bb = 0; bb < BB; ++bb) {
+      auto& sc = scs[bb];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float4 rec = smem_at<float4>(k_rec + (16 * bb + 8 * r) * 16);
+        const float4 rec = smem_at<float4>(st + k_rec + (16 * bb + 8 * r) * 16);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -665,12 +685,14 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     }
 
     // Weights, and P V for the 16 tokens of each block.
+    uint32_t pbs[BB][NB][2][2];    // [group][slots 0-7, 8-15]
 #pragma unroll
     for (int bb = 0; bb < BB; ++bb) {
-      uint32_t pb[NB][2][2];       // [group][slots 0-7, 8-15]
+      auto& pb = pbs[bb];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float4 rec = smem_at<float4>(v_rec + (16 * bb + 8 * r) * 16);
+        const float2 vs = smem_at<float2>(vs_rec + (16 * bb + 8 * r) * 8);
+        const uint32_t vb = smem_at<uint32_t>(vb_rec + (16 * bb + 8 * r) * 4);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           float e[2];
@@ -678,13 +700,17 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
           for (int c = 0; c < 2; ++c) {
             e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], -ref[nb][c]));
             l_run[nb][c] += e[c];
-            bias[nb][0][c] = fmaf(e[c], rec.y, bias[nb][0][c]);
-            bias[nb][1][c] = fmaf(e[c], rec.w, bias[nb][1][c]);
+            bias[nb][0][c] = fmaf(e[c], bf16_lo(vb), bias[nb][0][c]);
+            bias[nb][1][c] = fmaf(e[c], bf16_hi(vb), bias[nb][1][c]);
           }
-          pb[nb][0][r] = movmatrix_trans(pack_f16x2(e[0] * rec.x, e[1] * rec.x));
-          pb[nb][1][r] = movmatrix_trans(pack_f16x2(e[0] * rec.z, e[1] * rec.z));
+          pb[nb][0][r] = movmatrix_trans(pack_f16x2(e[0] * vs.x, e[1] * vs.x));
+          pb[nb][1][r] = movmatrix_trans(pack_f16x2(e[0] * vs.y, e[1] * vs.y));
         }
       }
+    }
+#pragma unroll
+    for (int bb = 0; bb < BB; ++bb) {
+      auto& pb = pbs[bb];
       // Slots 2 t4, 2 t4 + 1 and 8 more: this lane's tokens in V.
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

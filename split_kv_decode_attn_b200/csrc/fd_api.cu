@@ -719,10 +719,25 @@ fd_status decode_impl(const fd_problem* p, const void* q, const void* k_cache,
   return r;
 }
 
-// K + V bytes of one token of one KV head.
-double kv_token_bytes(int kv_dtype, int D) {
-  if (kv_dtype == FD_KV_INT4) return D + 16.0;   // D / 2 bytes of codes each, and the record
-  return 2.0 * D * (kv_dtype == FD_KV_FP8_E4M3 ? 1 : 2);
+// CTAs that a call over a 4-bit cache deals the batch to: as many as the SMs, if
+// the workspace of num_splits splits holds what they leave, two partial results
+// of G rows each and 16 bytes (the sum rounded up to 256 bytes before these).
+int int4_ctas(int num_sms, long long rows, int G, int D, int num_splits) {
+  const long long have = rows * G * num_splits * (D + 1) * 4 - 256;
+  const long long each = 2LL * G * (D + 1) * 4 + 16;
+  return static_cast<int>(std::clamp<long long>(have / each, 1, num_sms));
+}
+
+// The split count to ask for over a 4-bit cache: the least that fills the SMs.
+// One CTA per row, with no merge, is left for batches of at most one row per SM
+// whose histories hold no more than a unit of 64 tokens for each of a CTA's
+// eight warps.
+int plan_int4(int num_sms, long long rows, int G, int D, int longest) {
+  if (rows <= num_sms && longest <= 8 * fd::kTile) return 1;
+  const int S = static_cast<int>(std::clamp<long long>(2LL * num_sms / rows, 2, kMaxSplits));
+  for (int s = S; s < kMaxSplits; ++s)
+    if (int4_ctas(num_sms, rows, G, D, s) >= num_sms) return s;
+  return kMaxSplits;
 }
 
 // The planner over every input it uses.  seqlens: host lengths or null (every
@@ -732,7 +747,7 @@ int plan_impl(int num_sms, int B, int Hkv, int D, int max_len, int block_size, i
   // Two CTAs per slot from the batch alone: no split (this also bounds the
   // planning cost for large batches).
   if (static_cast<long long>(B) * Hkv >= 2LL * num_sms * fd::kCtasPerSm) return 1;
-  const PlanShape ps{num_sms, B, Hkv, kv_token_bytes(kv_dtype, D),
+  const PlanShape ps{num_sms, B, Hkv, 2.0 * D * (kv_dtype == FD_KV_FP8_E4M3 ? 1 : 2),
                      block_size > 0 && block_size < fd::kTile, D == 128,
                      kv_dtype == FD_KV_FP8_E4M3};
   const long long units = static_cast<long long>(B) * Hkv;
@@ -800,6 +815,11 @@ int fd_plan_problem(int num_sms, const fd_problem* p, const int32_t* seqlens) {
   if (num_sms < 1) {
     int dev = 0;
     if (current_device(&dev) != FD_OK || device_sms(dev, &num_sms) != FD_OK) return FD_ERR_CUDA;
+  }
+  if (p->kv_dtype == FD_KV_INT4) {
+    int longest = p->max_len;
+    if (seqlens) longest = std::min(longest, *std::max_element(seqlens, seqlens + p->B));
+    return plan_int4(num_sms, static_cast<long long>(p->B) * p->Hkv, p->Hq / p->Hkv, p->D, longest);
   }
   return plan_impl(num_sms, p->B, p->Hkv, p->D, p->max_len, p->block_size, p->kv_dtype, seqlens);
 }

@@ -222,9 +222,15 @@ __device__ __forceinline__ T smem_at(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
 }
 
+struct Int4Shared;
+
 struct Int4DecodeArgs {
-  SplitArgs a;            // as fd_split_kernel's; k_scale and v_scale do not apply
-  int prefetch_units;     // units per warp pulled into L2 before the wait on the previous grid
+  SplitArgs a;            // part_o [2 ctas, G, D] and part_lse [2 ctas, G]: see below; the
+                          // fields of the split cut, k_scale and v_scale do not apply
+  Int4Shared* shared;     // [ctas]
+  int B;
+  int ctas;               // CTAs the batch is dealt to (by_row: not used)
+  bool by_row;            // one CTA per (sequence, KV head), no partial results
 };
 
 // D = A B, m16n8k16, f16 inputs, fp32 result.
@@ -236,6 +242,113 @@ __device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+
+// ---- the cut.  The tokens of a (sequence, KV head) row are taken in units of U.
+// A row of n units costs n + 1: its end takes about as long as a unit (measured,
+// D = 128, G = 8: 1.9-2.0 us a unit, 2.2 us for the end of a row and the start of
+// the next).  The costs of all rows, one row after another, are dealt to the CTAs
+// in equal ranges, and a CTA's range to its warps.  A warp works through its
+// range alone, its copies running ahead over the ends of rows; nothing waits for
+// another warp before the range ends.  So the load is even whatever the lengths.
+// (One CTA per split of a row, as fd_split_kernel, left a ragged batch of 32 x up
+// to 8,192 tokens at 55-58 us whatever the split count and the CTAs' shape.)
+// CTA c of C begins at c T / C of the total cost T.
+//
+// Every warp works the cut out for itself from the lengths, whose first
+// kInt4Lens a CTA keeps in shared memory.  Costs stay below 2^31 (checked on the
+// host), so that c T / C = c (T / C) + c (T mod C) / C stays in 32 bits.
+constexpr int kInt4Lens = 512;
+
+__device__ __forceinline__ int int4_length(const SplitArgs& a, int b) {
+  return a.seqlens ? min(max(__ldcg(a.seqlens + b), 0), a.max_len) : a.max_len;
+}
+__device__ __forceinline__ int int4_length(const SplitArgs& a, const int* lens, int b) {
+  return b < kInt4Lens ? lens[b] : int4_length(a, b);
+}
+
+struct Int4Cut {
+  uint32_t total, ctas;     // cost; CTAs that get any
+  __device__ __forceinline__ uint32_t begin(uint32_t c) const {
+    return c * (total / ctas) + c * (total % ctas) / ctas;
+  }
+  // The CTA that holds place x: near x C / T, which is rounded in fp32.
+  __device__ __forceinline__ uint32_t holder(uint32_t x) const {
+    uint32_t c = min(static_cast<uint32_t>(static_cast<float>(x) * ctas / static_cast<float>(total)), ctas - 1);
+    while (begin(c) > x) --c;
+    while (begin(c + 1) <= x) ++c;
+    return c;
+  }
+};
+
+// Where a warp stands: unit u of the `units` of row (sequence b, KV head h),
+// whose sequence holds n tokens.
+struct Int4Walk {
+  int b, h, u, units, n;
+};
+
+// The place `at` (below the total): u == units at the end of a row.  rows: the
+// rows with a token before it.
+template <int U>
+__device__ __forceinline__ Int4Walk int4_locate(const SplitArgs& a, const int* lens, int B, int lane,
+                                                uint32_t at, uint32_t& rows) {
+  uint32_t before = 0, seqs = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int n = b0 + lane < B ? int4_length(a, lens, b0 + lane) : 0;
+    const int units = (n + U - 1) / U;
+    uint32_t sum = n > 0 ? static_cast<uint32_t>(units + 1) * a.Hkv : 0u;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += x;
+    }
+    const unsigned held = __ballot_sync(0xffffffffu, n > 0);
+    const unsigned hit = __ballot_sync(0xffffffffu, before + sum > at);
+    if (hit || b0 + 32 >= B) {
+      const int l = hit ? __ffs(hit) - 1 : 31;
+      Int4Walk w;
+      w.b = b0 + l;
+      w.n = __shfl_sync(0xffffffffu, n, l);
+      w.units = __shfl_sync(0xffffffffu, units, l);
+      const uint32_t off = at - (before + __shfl_sync(0xffffffffu, sum, l) - (w.units + 1) * a.Hkv);
+      w.h = static_cast<int>(off / (w.units + 1));
+      w.u = static_cast<int>(off) - w.h * (w.units + 1);
+      rows = (seqs + __popc(held & ((1u << l) - 1u))) * a.Hkv + w.h;
+      return w;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+    seqs += __popc(held);
+  }
+}
+
+// To the next unit; from the last one of a row to the next row that has any.
+template <int U>
+__device__ __forceinline__ void int4_advance(const SplitArgs& a, const int* lens, int B, Int4Walk& w) {
+  if (++w.u < w.units) return;
+  w.u = 0;
+  if (++w.h < a.Hkv) return;
+  w.h = 0;
+  do {
+    if (++w.b >= B) return;
+    w.n = int4_length(a, lens, w.b);
+  } while (w.n == 0);
+  w.units = (w.n + U - 1) / U;
+}
+
+// A state that a warp left: of row b Hkv + h (-1: none), which begins at place
+// `begin` of the batch's costs.
+struct Int4Piece {
+  long long row;
+  uint32_t begin, units;
+};
+static_assert(sizeof(Int4Piece) == 16, "as laid out in shared memory");
+
+// What a CTA leaves for the merge: the row that begins in its range and goes on
+// beyond (row -1: none), the number of CTAs that share it, and the index of its
+// first partial result.
+struct Int4Shared {
+  long long row;
+  int parts, first;
+};
 
 template <int D, int NB, class SH>
 struct Int4Smem {
@@ -250,16 +363,23 @@ struct Int4Smem {
   // then vb0, vb1 in bf16.  (K's part, in fp32, takes the records' place.)
   static constexpr int kVRecOffset = kInt4Warps * kWarpBytes;
   static constexpr int kVRecBytes = kUnit * 12;
-  static constexpr int kBarOffset = kVRecOffset + kInt4Warps * kVRecBytes;
-  static constexpr int kErrorOffset = kBarOffset + 8 * kInt4Warps * kInt4Stages;
-  static constexpr int kDynamicBytes = kErrorOffset + 16 + 1024;   // room to align to 1 KB
-  // A warp leaves its softmax state in its own drained ring (floats).
+  // A softmax state (floats): [column][kAccStride] outputs, the columns'
+  // references and sums.  A warp leaves up to two: that of the row its range
+  // begins in, in a place of its own, and that of the row its range ends in, over
+  // its drained ring.
   static constexpr int kNcol = NB * 8;
   static constexpr int kAccStride = D + 4;
   static constexpr int kM = kNcol * kAccStride;
   static constexpr int kL = kM + kNcol;
-  static constexpr int kWarpFloats = kWarpBytes / 4;
-  static_assert(kL + kNcol <= kWarpFloats, "the state of a warp fits its ring");
+  static constexpr int kStateFloats = kL + kNcol;
+  static_assert(kStateFloats * 4 <= kWarpBytes, "the state of a warp fits its ring");
+  static constexpr int kFirstOffset = kVRecOffset + kInt4Warps * kVRecBytes;
+  static constexpr int kRowOffset = kFirstOffset + kInt4Warps * kStateFloats * 4;   // Int4Piece[2 warps]
+  static constexpr int kLenOffset = kRowOffset + 2 * kInt4Warps * 16;
+  static constexpr int kBarOffset = kLenOffset + 4 * kInt4Lens;
+  static constexpr int kErrorOffset = kBarOffset + 8 * kInt4Warps * kInt4Stages;
+  static constexpr int kDynamicBytes = kErrorOffset + 16 + 1024;   // room to align to 1 KB
+  static_assert(kDynamicBytes <= 227 * 1024, "shared memory per CTA");
 };
 
 // Row of a unit's 16-token block that takes slot s (0..7) of the MMAs, 8..15
@@ -283,8 +403,12 @@ __device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
   return D == 128 ? a ^ ((r << 3) & 0x30u) : a ^ ((r << 2) & 0x10u);
 }
 
-// Split kernel of a 4-bit cache: one CTA per (split, KV head, sequence), as
-// fd_split_kernel, with the units of 32 tokens dealt to its warps in turn.
+// Decode attention over a 4-bit cache.  A row that lies within a warp's range is
+// finished by the warp, one within a CTA's by the CTA; of a row that goes over
+// the end of CTA c's range each CTA leaves one partial result, at index 2 c of
+// part_o and part_lse if the row began before the CTA's range (or with it),
+// otherwise at 2 c + 1; the CTA in which it begins names it in shared[c], and
+// fd_combine_int4_kernel merges the parts.
 //
 // No code is converted.  A nibble in the low four bits of a half word is the f16
 // subnormal c 2^-24 as it stands, one in the next four bits c 2^-20, both exact
@@ -322,7 +446,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   // The warp's number from a shuffle: the compiler then keeps what follows from
   // it, the addresses of copies and barriers, in uniform registers.
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -331,8 +454,9 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   const uint32_t ring_at = smem_u32(ring);
   const uint32_t bar = smem_u32(smem) + L::kBarOffset + 8 * kInt4Stages * warp;
   volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);
-  const int start = split_first_tile(a, split) * kTile;
-  const int split_end = split_first_tile(a, split + 1) * kTile;
+  Int4Piece* pieces = reinterpret_cast<Int4Piece*>(smem + L::kRowOffset);
+  const int B = p.B;
+  const bool paged = a.block_size != 0;
 
   if (lane == 0) {
     for (int s = 0; s < kInt4Stages; ++s) mbar_init(bar + 8 * s, 1);
@@ -340,93 +464,174 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
     prefetch_tensormap(&tmP);
+    pieces[2 * warp].row = pieces[2 * warp + 1].row = -1;
   }
   if (threadIdx.x == 0) *cta_error = 0;
-  if (lane < p.prefetch_units) {
-    // Only kernel arguments are used: the lengths may still be in flight.
-    const int t0 = start + (warp + lane * kInt4Warps) * kUnit;
-    if (t0 < min(split_end, a.max_len)) {
-      tma_prefetch_l2_4d(&tmK, kvh, t0, b);
-      tma_prefetch_l2_4d(&tmV, kvh, t0, b);
-      tma_prefetch_l2_4d(&tmP, kvh, t0, b);
+
+  __syncthreads();
+
+  // The lengths, and from them the range of this CTA and this warp's part of it.
+  // A first pass, before the wait on the previous grid, which may be writing the
+  // lengths, serves to pull the first units into L2 while that grid ends; it
+  // stands if the lengths read after the wait are the same.
+  int* lens = reinterpret_cast<int*>(smem + L::kLenOffset);
+  Int4Walk cur;
+  Int4Cut cut{0u, 0u};
+  uint32_t cta_begin = 0, cta_end = 0;
+  uint32_t row_begin = 0;              // where cur's row begins
+  int mine = 0;
+  if (p.by_row) {
+    grid_dependency_wait();
+    cur.b = blockIdx.y;
+    cur.h = blockIdx.x;
+    cur.n = int4_length(a, cur.b);
+    cur.units = (cur.n + kUnit - 1) / kUnit;
+    cta_end = cur.units;
+    cur.u = cur.units * warp / kInt4Warps;
+    mine = cur.units * (warp + 1) / kInt4Warps - cur.u;
+  } else {
+    for (int pass = 0; pass < 2; ++pass) {
+      bool changed = B > kInt4Lens;
+      if (pass == 1) grid_dependency_wait();
+      for (int b = threadIdx.x; b < min(B, kInt4Lens); b += kInt4Warps * 32) {
+        const int n = int4_length(a, b);
+        changed |= n != lens[b];
+        lens[b] = n;
+      }
+      if (pass == 1 ? !__syncthreads_or(changed) : (__syncthreads(), B > kInt4Lens)) {
+        if (pass == 1) break;
+        continue;
+      }
+      uint32_t total = 0, rows = 0;
+      for (int b = lane; b < B; b += 32) {
+        const int n = int4_length(a, lens, b);
+        if (n > 0) {
+          total += static_cast<uint32_t>((n + kUnit - 1) / kUnit + 1) * a.Hkv;
+          rows += a.Hkv;
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, off);
+        rows += __shfl_xor_sync(0xffffffffu, rows, off);
+      }
+      cut = Int4Cut{total, min(static_cast<uint32_t>(p.ctas), total)};
+      const bool any = blockIdx.x < cut.ctas;
+      cta_begin = any ? cut.begin(blockIdx.x) : 0u;
+      cta_end = any ? cut.begin(blockIdx.x + 1) : 0u;
+      const uint32_t cost = cta_end - cta_begin, each = cost / kInt4Warps, rest = cost % kInt4Warps;
+      const uint32_t lo = cta_begin + each * warp + rest * warp / kInt4Warps;
+      const uint32_t hi = cta_begin + each * (warp + 1) + rest * (warp + 1) / kInt4Warps;
+      mine = 0;
+      if (lo < hi) {
+        // Units before a place: its cost less the rows before it.
+        uint32_t rows_lo, rows_hi = rows;
+        cur = int4_locate<kUnit>(a, lens, B, lane, lo, rows_lo);
+        if (hi < total) int4_locate<kUnit>(a, lens, B, lane, hi, rows_hi);
+        mine = static_cast<int>((hi - rows_hi) - (lo - rows_lo));
+        row_begin = lo - cur.u;
+        if (cur.u == cur.units && mine > 0) {          // the end of a row: begin with the next
+          row_begin += cur.units + 1;
+          --cur.u;
+          int4_advance<kUnit>(a, lens, B, cur);
+        }
+      }
+      if (pass == 0 && !paged && mine > 0 && elect_one()) {
+        for (int i = 0; i < min(min(mine, kInt4Stages), cur.units - cur.u); ++i) {
+          tma_prefetch_l2_4d(&tmK, cur.h, (cur.u + i) * kUnit, cur.b);
+          tma_prefetch_l2_4d(&tmV, cur.h, (cur.u + i) * kUnit, cur.b);
+          tma_prefetch_l2_4d(&tmP, cur.h, (cur.u + i) * kUnit, cur.b);
+        }
+      }
     }
   }
-  __syncthreads();
-  grid_dependency_wait();
 
   // q's loads go ahead of the copies (behind them they took 2 us more to come
   // back): word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
-  const int h0 = kvh * a.G;
   uint4 raw[NB][2][KW];
+  auto load_q = [&]() {
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const bool live = nb * 8 + g < a.G;
-    const __nv_bfloat16* qrow = a.q + (static_cast<size_t>(b) * a.Hq + h0 + (live ? nb * 8 + g : 0)) * D;
+    for (int nb = 0; nb < NB; ++nb) {
+      const bool live = nb * 8 + g < a.G;
+      const __nv_bfloat16* qrow =
+          a.q + (static_cast<size_t>(cur.b) * a.Hq + cur.h * a.G + (live ? nb * 8 + g : 0)) * D;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        raw[nb][h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
-        if (!live) raw[nb][h][w] = make_uint4(0u, 0u, 0u, 0u);
-      }
-  }
-  const int n = seq_length(a.seqlens, b, a.max_len);
-  const int end = min(split_end, n);
-  const int n_parts = (a.n_splits == 1 || (n + kTile - 1) / kTile <= a.tile_q) ? 1 : 2;
-  if (start >= end) {
-    if (split == 0) {   // an empty sequence
-      const size_t base = (static_cast<size_t>(b) * a.Hq + h0) * D;
-      for (int i = threadIdx.x; i < a.G * D; i += kInt4Warps * 32) a.out[base + i] = __float2bfloat16_rn(0.f);
-      if (a.lse && threadIdx.x < a.G) a.lse[static_cast<size_t>(b) * a.Hq + h0 + threadIdx.x] = -INFINITY;
+        for (int w = 0; w < KW; ++w) {
+          raw[nb][h][w] = *reinterpret_cast<const uint4*>(qrow + h * (D / 2) + t4 * (D / 8) + 8 * w);
+          if (!live) raw[nb][h][w] = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
-    return;
-  }
-  const int n_units = (end - start + kUnit - 1) / kUnit;
-  const int mine = warp < n_units ? (n_units - warp + kInt4Warps - 1) / kInt4Warps : 0;
+  };
+  if (mine > 0) load_q();
 
-  // ---- copies: unit i of this warp holds tokens start + 32 (warp + 8 i) ..
+  // ---- copies, which run over the ends of rows
   const uint64_t policy = policy_evict_first();
-  const bool paged = a.block_size != 0;
   const int lbs = a.log2_block_size;
   const int pages_per_unit = paged && a.block_size < kUnit ? kUnit >> lbs : 1;
   const int box_rows = kUnit / pages_per_unit;
-  const int n_pages = paged ? (n + a.block_size - 1) >> lbs : 0;
-  const int32_t* table = a.block_table + static_cast<size_t>(b) * a.max_blocks_per_seq;
-  auto unit_token = [&](int i) { return start + (warp + i * kInt4Warps) * kUnit; };
-  // The page of this lane's box in unit i (lanes past the boxes: none).
-  auto page_of = [&](int i) {
-    const int pg = (unit_token(i) >> lbs) + lane;
-    return paged && i < mine && lane < pages_per_unit && pg < n_pages ? __ldg(table + pg) : 0;
+  Int4Walk ahead = cur;                                // the unit to be copied next
+  // The page of this lane's box in that unit (lanes past the boxes: none).
+  auto page_ahead = [&]() {
+    const int pg = ((ahead.u * kUnit) >> lbs) + lane;
+    return paged && lane < pages_per_unit && pg < ((ahead.n + a.block_size - 1) >> lbs)
+               ? __ldg(a.block_table + static_cast<size_t>(ahead.b) * a.max_blocks_per_seq + pg)
+               : 0;
   };
-  int next_page = page_of(0);
-  auto issue = [&](int i, uint32_t s) {                // into stage s
-    const int t0 = unit_token(i);
+  int issued = 0;
+  int next_page = mine > 0 ? page_ahead() : 0;
+  auto issue = [&](uint32_t s) {                       // into stage s
+    const int t0 = ahead.u * kUnit;
     const uint32_t st = ring_at + s * L::kStageBytes;
     const uint32_t full = bar + 8 * s;
     if (!paged) {
       if (elect_one()) {
         mbar_arrive_expect_tx(full, kUnit * (D + 16));
-        tma_load_4d(st, &tmK, full, kvh, t0, b, policy);
-        tma_load_4d(st + L::kV, &tmV, full, kvh, t0, b, policy);
-        tma_load_4d(st + L::kP, &tmP, full, kvh, t0, b, policy);
+        tma_load_4d(st, &tmK, full, ahead.h, t0, ahead.b, policy);
+        tma_load_4d(st + L::kV, &tmV, full, ahead.h, t0, ahead.b, policy);
+        tma_load_4d(st + L::kP, &tmP, full, ahead.h, t0, ahead.b, policy);
       }
     } else {
-      const int boxes = min(pages_per_unit, n_pages - (t0 >> lbs));
+      const int boxes = min(pages_per_unit, ((ahead.n + a.block_size - 1) >> lbs) - (t0 >> lbs));
       if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (D + 16));
       __syncwarp();
       if (lane < boxes) {
         const int row = t0 & (a.block_size - 1);
         const uint32_t r = lane * box_rows;
-        tma_load_4d(st + r * L::kRowBytes, &tmK, full, kvh, row, next_page, policy);
-        tma_load_4d(st + L::kV + r * L::kRowBytes, &tmV, full, kvh, row, next_page, policy);
-        tma_load_4d(st + L::kP + r * 16, &tmP, full, kvh, row, next_page, policy);
+        tma_load_4d(st + r * L::kRowBytes, &tmK, full, ahead.h, row, next_page, policy);
+        tma_load_4d(st + L::kV + r * L::kRowBytes, &tmV, full, ahead.h, row, next_page, policy);
+        tma_load_4d(st + L::kP + r * 16, &tmP, full, ahead.h, row, next_page, policy);
       }
-      next_page = page_of(i + 1);
+    }
+    if (++issued < mine) {
+      int4_advance<kUnit>(a, lens, B, ahead);
+      next_page = page_ahead();
     }
   };
-  int issued = 0;
-  for (; issued < min(mine, kInt4Stages); ++issued) issue(issued, issued);
+  while (issued < min(mine, kInt4Stages)) issue(issued);
 
+  // Offsets within a unit of this lane's loads: codes of K (slot g), of V
+  // (slots 2 t4 and 2 t4 + 1) and the records of slot g.
+  constexpr uint32_t kEight = 8 * L::kRowBytes;        // 8 rows further
+  const uint32_t k_row = int4_slot_row<D>(g);
+  uint32_t k_at[2], v_at[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    k_at[h] = int4_code_offset<D>(k_row, h * (D / 4) + t4 * (D / 16));
+    v_at[h][0] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4), h * (D / 4) + g * (D / 32));
+    v_at[h][1] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4 + 1), h * (D / 4) + g * (D / 32));
+  }
+  const uint32_t k_rec = L::kP + k_row * 16;           // within the unit
+  uint8_t* v_recs = smem + L::kVRecOffset + warp * L::kVRecBytes;
+  const uint8_t* vs_rec = v_recs + k_row * 8;
+  const uint8_t* vb_rec = v_recs + kUnit * 8 + k_row * 4;
+  bool failed = false;
+  uint32_t stage = 0, phase = 0;
+
+  for (int done = 0; done < mine && !failed;) {        // the rows of the range
+  const int u_first = cur.u;
+  const int count = min(cur.units - cur.u, mine - done);
   // ---- q in f16, in the order of K's codes: k-step s of a word takes nibbles
   // 2s, 2s+4 (slots 2 t4, 2 t4 + 1) and 2s+1, 2s+5 (slots 2 t4 + 8, + 9).
   uint32_t qf[NB][2][KW][2][2];
@@ -505,31 +710,14 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
         for (int j = 0; j < MB; ++j) acc[nb][h][j][i] = 0.f;
     }
 
-  // Offsets within a unit of this lane's loads: codes of K (slot g), of V
-  // (slots 2 t4 and 2 t4 + 1) and the record of slot g.
-  constexpr uint32_t kEight = 8 * L::kRowBytes;        // 8 rows further
-  const uint32_t k_row = int4_slot_row<D>(g);
-  uint32_t k_at[2], v_at[2][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    k_at[h] = int4_code_offset<D>(k_row, h * (D / 4) + t4 * (D / 16));
-    v_at[h][0] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4), h * (D / 4) + g * (D / 32));
-    v_at[h][1] = L::kV + int4_code_offset<D>(int4_slot_row<D>(2 * t4 + 1), h * (D / 4) + g * (D / 32));
-  }
-  const uint32_t k_rec = L::kP + k_row * 16;           // within the unit
-  uint8_t* v_recs = smem + L::kVRecOffset + warp * L::kVRecBytes;
-  const uint8_t* vs_rec = v_recs + k_row * 8;
-  const uint8_t* vb_rec = v_recs + kUnit * 8 + k_row * 4;
-  bool failed = false;
-  uint32_t stage = 0, phase = 0;
-  for (int i = 0; i < mine; ++i) {
+  for (int i = 0; i < count; ++i) {
     uint8_t* st = ring + stage * L::kStageBytes;
     const bool ok = mbar_wait(bar + 8 * stage, phase, kWaitLimitNs);
     if (!__all_sync(0xffffffffu, ok)) {
       failed = true;
       break;
     }
-    const int valid = end - unit_token(i);             // tokens of the unit that count
+    const int valid = cur.n - (u_first + i) * kUnit;   // tokens of the unit that count
 
     // Records unpacked, one token per lane and 32 tokens: K's as ks0, kb0 - 8 ks0,
     // ks1, kb1 - 8 ks1 in fp32 over the record, V's beside the ring; zeros for a
@@ -743,26 +931,23 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
         for (int nb = 0; nb < NB; ++nb) mma_f16_16816(eight[nb], v8, pb[nb][h][0], pb[nb][h][1]);
       }
     }
-    __syncwarp();                                      // the stage is read: refill it
-    if (issued < mine) issue(issued++, stage);
+    // The stage is read (and its records were written to): refill it.
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (issued < mine) issue(stage);
     if (++stage == kInt4Stages) {
       stage = 0;
       phase ^= 1;
     }
   }
-  grid_dependents_launch();
-  if (failed && lane == 0) {
-    raise_device_error(1u);
-    *cta_error = 1;
-    // No copy may still be landing in shared memory when the CTA retires.
-    for (int i = issued > kInt4Stages ? issued - kInt4Stages : 0; i < issued; ++i)
-      if (!mbar_wait(bar + 8 * (i % kInt4Stages), (i / kInt4Stages) & 1, kWaitLimitNs)) raise_device_error(2u);
-  }
-  __syncwarp();
+  if (failed) break;
 
-  // ---- merge of the warps' states.  Row g of m-block j of group h is entry
+  // ---- the row's end within the range.  Row g of m-block j of group h is entry
   // h D/2 + g D/16 + 2 j, row g + 8 the next one.
-  float* f = reinterpret_cast<float*>(smem) + warp * L::kWarpFloats;
+  const bool whole = u_first == 0 && count == cur.units;
+  const bool is_first = done == 0;
+  float* f = reinterpret_cast<float*>(is_first ? smem + L::kFirstOffset + warp * L::kStateFloats * 4 : ring);
+  if (!whole && !is_first) __syncwarp();               // the ring is drained, and read by every lane
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -774,61 +959,213 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
         bias[nb][1][c] += __shfl_xor_sync(0xffffffffu, bias[nb][1][c], off);
       }
       const int col = nb * 8 + 2 * t4 + c;
+      const size_t orow = static_cast<size_t>(cur.b) * a.Hq + cur.h * a.G + col;
+      const float inv = l_run[nb][c] == 0.f ? 0.f : 1.f / l_run[nb][c];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float r = 1.f / inv_r[h], r0 = r * 0x1p24f, r1 = r * 0x1p20f;
         const float w8 = eight[nb][2 * h + c];
-        float* o = f + col * L::kAccStride + h * (D / 2) + g * (D / 16);
+        const int d = h * (D / 2) + g * (D / 16);
+        float o[2 * MB];
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
-          *reinterpret_cast<float2*>(o + 2 * j) =
-              make_float2(fmaf(acc[nb][h][j][c] - w8, r0, bias[nb][h][c]),
-                          fmaf(acc[nb][h][j][c + 2] - 16.f * w8, r1, bias[nb][h][c]));
+        for (int j = 0; j < MB; ++j) {
+          o[2 * j] = fmaf(acc[nb][h][j][c] - w8, r0, bias[nb][h][c]);
+          o[2 * j + 1] = fmaf(acc[nb][h][j][c + 2] - 16.f * w8, r1, bias[nb][h][c]);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 2 * MB; j += 4)
+            *reinterpret_cast<float4*>(f + col * L::kAccStride + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        } else if (col < a.G) {
+          uint32_t w[MB];
+#pragma unroll
+          for (int j = 0; j < MB; ++j) w[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+          if constexpr (MB == 4)
+            *reinterpret_cast<uint4*>(a.out + orow * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+          else
+            *reinterpret_cast<uint2*>(a.out + orow * D + d) = make_uint2(w[0], w[1]);
+        }
       }
       if (g == 0) {
-        f[L::kM + col] = bound[nb][c] == -INFINITY && l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
-        f[L::kL + col] = l_run[nb][c];
+        if (!whole) {
+          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
+          f[L::kL + col] = l_run[nb][c];
+        } else if (col < a.G && a.lse) {
+          a.lse[orow] = (ref[nb][c] + log2f(l_run[nb][c])) * 0.69314718055994530942f;
+        }
       }
     }
-  __syncthreads();
-  if (*cta_error) return;
-  const float* all = reinterpret_cast<const float*>(smem);
-  constexpr int kChunks = D / 4;
-  for (int c = threadIdx.x; c < a.G * kChunks; c += kInt4Warps * 32) {
-    const int hd = c / kChunks, d = (c % kChunks) * 4;
-    float m[kInt4Warps], M = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kInt4Warps; ++w) {
-      m[w] = all[w * L::kWarpFloats + L::kM + hd];
-      M = fmaxf(M, m[w]);
-    }
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kInt4Warps; ++w) {
-      if (m[w] == -INFINITY) continue;                 // no token
-      const float wt = ex2(m[w] - M);
-      const float4 v = *reinterpret_cast<const float4*>(all + w * L::kWarpFloats + hd * L::kAccStride + d);
-      l += wt * all[w * L::kWarpFloats + L::kL + hd];
-      o.x += wt * v.x;
-      o.y += wt * v.y;
-      o.z += wt * v.z;
-      o.w += wt * v.w;
-    }
-    const float inv = 1.f / l;
-    const float lse = (M + log2f(l)) * 0.69314718055994530942f;
-    const size_t row = static_cast<size_t>(b) * a.Hq + h0 + hd;
-    if (n_parts == 1) {
-      *reinterpret_cast<uint2*>(a.out + row * D + d) =
-          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-      if (d == 0 && a.lse) a.lse[row] = lse;
-    } else {
-      *reinterpret_cast<float4*>(a.part_o + (row * a.n_splits + split) * D + d) =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      // The merge takes a row whose partials are all NaN as empty; +inf makes
-      // it NaN, as rows of NaN have to.
-      if (d == 0) a.part_lse[row * a.n_splits + split] = lse != lse ? INFINITY : lse;
+  if (!whole && lane == 0) {
+    Int4Piece& pc = pieces[2 * warp + (is_first ? 0 : 1)];
+    pc.row = static_cast<long long>(cur.b) * a.Hkv + cur.h;
+    pc.begin = row_begin;
+    pc.units = cur.units;
+  }
+  done += count;
+  if (done < mine) {
+    row_begin += cur.units + 1;
+    cur.u += count - 1;
+    int4_advance<kUnit>(a, lens, B, cur);
+    load_q();
+  }
+  }
+  grid_dependents_launch();
+  if (failed && lane == 0) {
+    raise_device_error(1u);
+    *cta_error = 1;
+    // No copy may still be landing in shared memory when the CTA retires: the
+    // copies in flight are the last ones issued, in the stages from `stage` on.
+    for (int i = 0; i < kInt4Stages; ++i) {
+      if (!mbar_wait(bar + 8 * stage, phase, kWaitLimitNs)) raise_device_error(2u);
+      if (++stage == kInt4Stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
   }
+  // Sequences without a token belong to no range.
+  if (!p.by_row || cta_end == 0) {
+    for (int b = p.by_row ? blockIdx.y : blockIdx.x; b < B; b += p.by_row ? B : gridDim.x) {
+      if ((p.by_row ? cur.n : int4_length(a, lens, b)) > 0) continue;
+      const int rows = p.by_row ? a.G : a.Hq;
+      const size_t row = static_cast<size_t>(b) * a.Hq + (p.by_row ? blockIdx.x * a.G : 0);
+      for (int i = threadIdx.x; i < rows * D; i += kInt4Warps * 32) a.out[row * D + i] = __float2bfloat16_rn(0.f);
+      if (a.lse)
+        for (int i = threadIdx.x; i < rows; i += kInt4Warps * 32) a.lse[row + i] = -INFINITY;
+    }
+  }
+  __syncthreads();
+  if (*cta_error) return;
+
+  // ---- rows that several warps share, one after another.  Lane k of each warp
+  // looks at piece k; the pieces of a row are neighbours.
+  constexpr int kPieces = 2 * kInt4Warps;
+  static_assert(kPieces <= 32, "a lane per piece");
+  const long long my_row = lane < kPieces ? pieces[lane].row : -1;
+  unsigned todo = __ballot_sync(0xffffffffu, my_row >= 0);
+  Int4Shared sh{-1, 0, 0};
+  while (todo) {
+    const int k0 = __ffs(todo) - 1;
+    const long long row = __shfl_sync(0xffffffffu, my_row, k0);
+    const unsigned held = __ballot_sync(0xffffffffu, my_row == row);
+    todo &= ~held;
+    const uint32_t begin = pieces[k0].begin, end = begin + pieces[k0].units;
+    const bool whole = begin >= cta_begin && end <= cta_end;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (begin > cta_begin ? 1 : 0);
+    if (!whole && begin >= cta_begin)
+      sh = Int4Shared{row, static_cast<int>(cut.holder(end - 1) - blockIdx.x) + 1, slot};
+    constexpr int kChunks = D / 4;
+    for (int c = threadIdx.x; c < a.G * kChunks; c += kInt4Warps * 32) {
+      const int hd = c / kChunks, d = (c % kChunks) * 4;
+      const float* states = reinterpret_cast<const float*>(smem);
+      float m[kPieces], M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int at = (k & 1) ? (k >> 1) * (L::kWarpBytes / 4) : L::kFirstOffset / 4 + (k >> 1) * L::kStateFloats;
+        m[k] = (held >> k) & 1u ? states[at + L::kM + hd] : -INFINITY;
+        M = fmaxf(M, m[k]);
+      }
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int at = (k & 1) ? (k >> 1) * (L::kWarpBytes / 4) : L::kFirstOffset / 4 + (k >> 1) * L::kStateFloats;
+        if ((held >> k) & 1u) {
+          const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M);
+          const float4 v = *reinterpret_cast<const float4*>(states + at + hd * L::kAccStride + d);
+          l += wt * states[at + L::kL + hd];
+          o.x += wt * v.x;
+          o.y += wt * v.y;
+          o.z += wt * v.z;
+          o.w += wt * v.w;
+        }
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse = (M + log2f(l)) * 0.69314718055994530942f;
+      if (whole) {
+        // Rows are numbered b Hkv + h, queries b Hq + h G + head.
+        const size_t orow = static_cast<size_t>(row) * a.G + hd;
+        *reinterpret_cast<uint2*>(a.out + orow * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (d == 0 && a.lse) a.lse[orow] = lse;
+      } else {
+        const size_t prow = static_cast<size_t>(slot) * a.G + hd;
+        *reinterpret_cast<float4*>(a.part_o + prow * D + d) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (d == 0) a.part_lse[prow] = lse;
+      }
+    }
+  }
+  if (gridDim.x > 1 && !p.by_row && threadIdx.x == 0) p.shared[blockIdx.x] = sh;
+}
+
+constexpr int kInt4CombineWarps = 4;
+
+// Merges the partial results of rows that several CTAs share: one warp per (CTA,
+// query head of a group), which takes the row that begins in the CTA's range, its
+// lanes over D.
+template <int D>
+__global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel(const Int4DecodeArgs p) {
+  constexpr int VPL = D / 32, BATCH = 16;
+  const SplitArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int w = blockIdx.x * kInt4CombineWarps + (threadIdx.x >> 5);
+  const int cta = w / a.G, head = w - cta * a.G;
+  grid_dependency_wait();     // partial results come from the kernel before
+  grid_dependents_launch();
+  if (cta >= p.ctas) return;
+  const long long row = __ldcg(&p.shared[cta].row);
+  const int parts = __ldcg(&p.shared[cta].parts), first = __ldcg(&p.shared[cta].first);
+  if (row < 0) return;
+  const size_t r = static_cast<size_t>(row) * a.G + head;
+  auto index = [&](int i) {            // of part i
+    return static_cast<size_t>(i == 0 ? first : 2 * (cta + i)) * a.G + head;
+  };
+  constexpr float kLog2e = 1.4426950408889634074f;
+  float mx = -INFINITY;
+  bool nan = false;
+  for (int i = lane; i < parts; i += 32) {
+    const float l = __ldcg(a.part_lse + index(i));
+    nan |= l != l;
+    mx = fmaxf(mx, l);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  if (__any_sync(0xffffffffu, nan)) mx = NAN;          // rows of NaN give NaN
+  float W = 0.f, acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  for (int s = 0; s < parts; s += BATCH) {
+    float lb[BATCH], ob[BATCH][VPL];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+      if (s + j < parts) {
+        const size_t x = index(s + j);
+        lb[j] = __ldcg(a.part_lse + x);
+        if constexpr (VPL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + x * D) + lane);
+          ob[j][0] = v.x; ob[j][1] = v.y; ob[j][2] = v.z; ob[j][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + x * D) + lane);
+          ob[j][0] = v.x; ob[j][1] = v.y;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+      if (s + j < parts) {
+        const float w = mx == -INFINITY ? 0.f : ex2((lb[j] - mx) * kLog2e);
+        W += w;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) acc[i] += w * ob[j][i];
+      }
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;
+  if constexpr (VPL == 4)
+    *reinterpret_cast<uint2*>(a.out + r * D + lane * 4) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(a.out + r * D + lane * 2) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (a.lse && lane == 0) a.lse[r] = mx + logf(W);
 }
 
 }  // namespace fd

@@ -14,6 +14,7 @@ fd_status int4_cache(const fd_problem* p, const void* k4, const void* v4, const 
   if (st != FD_OK) return st;
   if (p->kv_layout != FD_LAYOUT_HND && p->kv_layout != FD_LAYOUT_NHD) return FD_ERR_INVALID_ARGUMENT;
   if (p->kv_dtype != FD_KV_INT4) return FD_ERR_INVALID_ARGUMENT;
+  if (p->max_len > 0x7fffff00) return FD_ERR_INVALID_ARGUMENT;   // lengths are rounded up in int32
   if (p->block_size != 0) {
     if (p->num_blocks < 1 || p->max_blocks_per_seq < 1) return FD_ERR_INVALID_ARGUMENT;
     if (static_cast<long long>(p->max_blocks_per_seq) * p->block_size < p->max_len)
@@ -235,15 +236,9 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(seqlens, 4) || !aligned(block_table, 4))
     return FD_ERR_INVALID_ARGUMENT;
-  const Chunking chunks = chunking(p->max_len, num_splits);
   fd::SplitArgs& a = d.a;
-  if (chunks.splits > 1) {
-    const size_t need = fd_workspace_bytes(p->B, p->Hq, p->D, chunks.splits);
-    if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE;
-    const size_t rows = static_cast<size_t>(p->B) * p->Hq * chunks.splits;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(rows * p->D * 4));
-  }
+  const size_t need = fd_workspace_bytes(p->B, p->Hq, p->D, num_splits);
+  if (num_splits > 1 && (!workspace || workspace_bytes < need)) return FD_ERR_WORKSPACE;
   int dev = 0;
   const fd_status arch = this_device(&dev);
   if (arch != FD_OK) return arch;
@@ -265,16 +260,25 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.block_size = p->block_size;
   a.log2_block_size = p->block_size ? ilog2(p->block_size) : 0;
   a.max_blocks_per_seq = p->max_blocks_per_seq;
-  a.tiles = chunks.tiles;
-  a.n_splits = chunks.splits;
-  a.tile_q = chunks.tiles / chunks.splits;
-  a.tile_r = chunks.tiles % chunks.splits;
   a.scale_log2 = scale * 1.4426950408889634074f;
   a.scale = scale;
-  d.prefetch_units = p->block_size ? 0 : 3;
-  const dim3 grid(static_cast<unsigned>(chunks.splits), static_cast<unsigned>(p->Hkv),
-                  static_cast<unsigned>(p->B));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  d.B = p->B;
+  // Two partial results per CTA, and what the merge needs to know of it, have to
+  // fit the workspace; more than one CTA per SM would wait for a place.
+  int sms = 0;
+  if (device_sms(dev, &sms) != FD_OK) return FD_ERR_CUDA;
+  const long long rows = static_cast<long long>(p->B) * p->Hkv;
+  if (rows * ((p->max_len + unit - 1LL) / unit + 1) > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
+  d.by_row = num_splits == 1;
+  if (!d.by_row) {
+    d.ctas = int4_ctas(sms, rows, a.G, p->D, num_splits);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_lse = a.part_o + static_cast<size_t>(2) * d.ctas * a.G * p->D;
+    d.shared = reinterpret_cast<fd::Int4Shared*>(static_cast<char*>(workspace) +
+                                                 round256(static_cast<size_t>(2) * d.ctas * a.G * (p->D + 1) * 4));
+  }
+  const dim3 grid = d.by_row ? dim3(static_cast<unsigned>(p->Hkv), static_cast<unsigned>(p->B))
+                             : dim3(static_cast<unsigned>(d.ctas));
   fd_status r;
   if (p->D == 128)
     r = a.G <= 8 ? launch_split_int4<128, 1, ShapeN>(maps, d, grid, dev, stream)
@@ -282,8 +286,12 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   else
     r = a.G <= 8 ? launch_split_int4<64, 1, ShapeN>(maps, d, grid, dev, stream)
                  : launch_split_int4<64, 2, ShapeW>(maps, d, grid, dev, stream);
-  if (r == FD_OK && chunks.splits > 1)
-    r = p->D == 128 ? launch_combine<128>(a, p->B, s) : launch_combine<64>(a, p->B, s);
+  if (r == FD_OK && !d.by_row && d.ctas > 1) {
+    const dim3 cgrid(static_cast<unsigned>((d.ctas * a.G + fd::kInt4CombineWarps - 1) / fd::kInt4CombineWarps));
+    const int threads = fd::kInt4CombineWarps * 32;
+    r = p->D == 128 ? launch_chained(fd::fd_combine_int4_kernel<128>, cgrid, threads, 0, stream, d)
+                    : launch_chained(fd::fd_combine_int4_kernel<64>, cgrid, threads, 0, stream, d);
+  }
   return r;
 }
 

@@ -265,17 +265,43 @@ def test_a_history_of_nan_rows_alone_is_nan():
         assert torch().isnan(out).all() and torch().isnan(lse).all()
 
 
-def test_repeated_calls_and_batch_mates_give_the_same_bits():
+def test_repeated_calls_give_the_same_bits():
     t = torch()
-    c = Cache([900, 333, 1200, 5], 32, 4, 128, 1200, seed=700).on_device()
-    a = decode(c, 4)
-    for _ in range(3):
-        b = decode(c, 4)
-        assert t.equal(a[0], b[0]) and t.equal(a[1], b[1])
-    one = Cache([900], 32, 4, 128, 1200, seed=700, k=c.k[:1], v=c.v[:1])
-    one.q = c.q[:1]
-    b = decode(one.on_device(), 4)
-    assert t.equal(a[0][:1], b[0]) and t.equal(a[1][:1], b[1])
+    for S in (1, 2, 4, 37):
+        c = Cache([900, 333, 1200, 5, 0, 64], 32, 4, 128, 1200, seed=700).on_device()
+        a = decode(c, S)
+        for _ in range(3):
+            b = decode(c, S)
+            assert t.equal(a[0], b[0]) and t.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("B", [1, 31, 33, 70, 300])
+def test_ragged_batches_and_ranges_that_end_anywhere(B):
+    """Ranges of CTAs and of warps that begin and end inside rows, at their
+    edges, hold many rows or part of one; empty sequences at the front, at the
+    end and in between."""
+    r = np.random.default_rng(B)
+    lens = r.integers(0, 260, B)
+    lens[r.random(B) < 0.3] = 0
+    if B > 1:
+        lens[0] = lens[-1] = 0
+        lens[B // 2] = 1500
+    else:
+        lens[:] = 1500
+    for Hkv, G, D in ((1, 4, 64), (3, 8, 128), (2, 16, 64)):
+        c = Cache(list(lens), Hkv * G, Hkv, D, 1500, seed=800 + B).on_device()
+        ref = c.oracle()
+        for S in (1, 2, 3, 16, 300):
+            check(*decode(c, S), ref, f"B={B} Hkv={Hkv} G={G} S={S}")
+
+
+def test_ranges_that_end_with_rows():
+    """Rows of 1, 2, 4 and 8 units: the ranges' ends fall on the rows' ends."""
+    for n in (64, 128, 256, 512, 2048):
+        c = Cache([n] * 4, 8, 1, 128, n, seed=850 + n).on_device()
+        ref = c.oracle()
+        for S in (1, 2, 4, 8, 16, 64):
+            check(*decode(c, S), ref, f"n={n} S={S}")
 
 
 def test_two_streams_and_a_stream_that_is_not_current():

@@ -720,24 +720,19 @@ fd_status decode_impl(const fd_problem* p, const void* q, const void* k_cache,
 }
 
 // CTAs that a call over a 4-bit cache deals the batch to: as many as the SMs, if
-// the workspace of num_splits splits holds what they leave, two partial results
-// of G rows each and 16 bytes (the sum rounded up to 256 bytes before these).
-int int4_ctas(int num_sms, long long rows, int G, int D, int num_splits) {
-  const long long have = rows * G * num_splits * (D + 1) * 4 - 256;
-  const long long each = 2LL * G * (D + 1) * 4 + 16;
-  return static_cast<int>(std::clamp<long long>(have / each, 1, num_sms));
+// the workspace of num_splits splits (B Hq num_splits rows) holds what they leave,
+// two partial results of G rows each.
+int int4_ctas(int num_sms, long long rows, int num_splits) {
+  return static_cast<int>(std::clamp<long long>(rows * num_splits / 2, 1, num_sms));
 }
 
 // The split count to ask for over a 4-bit cache: the least that fills the SMs.
 // One CTA per row, with no merge, is left for batches of at most one row per SM
 // whose histories hold no more than a unit of 64 tokens for each of a CTA's
 // eight warps.
-int plan_int4(int num_sms, long long rows, int G, int D, int longest) {
+int plan_int4(int num_sms, long long rows, int longest) {
   if (rows <= num_sms && longest <= 8 * fd::kTile) return 1;
-  const int S = static_cast<int>(std::clamp<long long>(2LL * num_sms / rows, 2, kMaxSplits));
-  for (int s = S; s < kMaxSplits; ++s)
-    if (int4_ctas(num_sms, rows, G, D, s) >= num_sms) return s;
-  return kMaxSplits;
+  return static_cast<int>(std::clamp<long long>((2LL * num_sms + rows - 1) / rows, 2, kMaxSplits));
 }
 
 // The planner over every input it uses.  seqlens: host lengths or null (every
@@ -819,7 +814,7 @@ int fd_plan_problem(int num_sms, const fd_problem* p, const int32_t* seqlens) {
   if (p->kv_dtype == FD_KV_INT4) {
     int longest = p->max_len;
     if (seqlens) longest = std::min(longest, *std::max_element(seqlens, seqlens + p->B));
-    return plan_int4(num_sms, static_cast<long long>(p->B) * p->Hkv, p->Hq / p->Hkv, p->D, longest);
+    return plan_int4(num_sms, static_cast<long long>(p->B) * p->Hkv, longest);
   }
   return plan_impl(num_sms, p->B, p->Hkv, p->D, p->max_len, p->block_size, p->kv_dtype, seqlens);
 }

@@ -191,7 +191,7 @@ struct Int4Shape {
 constexpr float kRescaleLog2 = 8.f;   // a score may pass the reference by 2^8 ...
 constexpr float kWeightLog2 = 7.f;    // ... whose own weight is 2^7
 
-// 4-D tile load and L2 prefetch: {byte, head, row, plane}.
+// 4-D tile load: {byte, head, row, plane}.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, uint32_t bar,
                                             int head, int row, int plane, uint64_t policy) {
   asm volatile(
@@ -200,14 +200,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(0), "r"(head), "r"(row), "r"(plane),
       "l"(policy)
       : "memory");
-}
-
-__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* tm, int head, int row,
-                                                   int plane) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(tm)),
-               "r"(0), "r"(head), "r"(row), "r"(plane)
-               : "memory");
 }
 
 // True in one lane of a converged warp.
@@ -222,15 +214,13 @@ __device__ __forceinline__ T smem_at(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
 }
 
-struct Int4Shared;
-
 struct Int4DecodeArgs {
   SplitArgs a;            // part_o [2 ctas, G, D] and part_lse [2 ctas, G]: see below; the
                           // fields of the split cut, k_scale and v_scale do not apply
-  Int4Shared* shared;     // [ctas]
   int B;
   int ctas;               // CTAs the batch is dealt to (by_row: not used)
   bool by_row;            // one CTA per (sequence, KV head), no partial results
+  bool evict_first;       // what is read leaves L2 first
 };
 
 // D = A B, m16n8k16, f16 inputs, fp32 result.
@@ -342,14 +332,6 @@ struct Int4Piece {
 };
 static_assert(sizeof(Int4Piece) == 16, "as laid out in shared memory");
 
-// What a CTA leaves for the merge: the row that begins in its range and goes on
-// beyond (row -1: none), the number of CTAs that share it, and the index of its
-// first partial result.
-struct Int4Shared {
-  long long row;
-  int parts, first;
-};
-
 template <int D, int NB, class SH>
 struct Int4Smem {
   static constexpr int kUnit = SH::UNIT, kInt4Warps = SH::WARPS, kInt4Stages = SH::STAGES;
@@ -407,8 +389,7 @@ __device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
 // finished by the warp, one within a CTA's by the CTA; of a row that goes over
 // the end of CTA c's range each CTA leaves one partial result, at index 2 c of
 // part_o and part_lse if the row began before the CTA's range (or with it),
-// otherwise at 2 c + 1; the CTA in which it begins names it in shared[c], and
-// fd_combine_int4_kernel merges the parts.
+// otherwise at 2 c + 1, and fd_combine_int4_kernel merges them.
 //
 // No code is converted.  A nibble in the low four bits of a half word is the f16
 // subnormal c 2^-24 as it stands, one in the next four bits c 2^-20, both exact
@@ -470,10 +451,12 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
 
   __syncthreads();
 
+  grid_dependency_wait();
+
   // The lengths, and from them the range of this CTA and this warp's part of it.
-  // A first pass, before the wait on the previous grid, which may be writing the
-  // lengths, serves to pull the first units into L2 while that grid ends; it
-  // stands if the lengths read after the wait are the same.
+  // (Working it out ahead of the wait on the lengths as they stood, to pull the
+  // first units into L2, and again if they had changed, gained 0.7 us on batches
+  // of a few short sequences and lost 0.8-1.4 us on every larger one.)
   int* lens = reinterpret_cast<int*>(smem + L::kLenOffset);
   Int4Walk cur;
   Int4Cut cut{0u, 0u};
@@ -481,7 +464,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   uint32_t row_begin = 0;              // where cur's row begins
   int mine = 0;
   if (p.by_row) {
-    grid_dependency_wait();
     cur.b = blockIdx.y;
     cur.h = blockIdx.x;
     cur.n = int4_length(a, cur.b);
@@ -490,58 +472,40 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     cur.u = cur.units * warp / kInt4Warps;
     mine = cur.units * (warp + 1) / kInt4Warps - cur.u;
   } else {
-    for (int pass = 0; pass < 2; ++pass) {
-      bool changed = B > kInt4Lens;
-      if (pass == 1) grid_dependency_wait();
-      for (int b = threadIdx.x; b < min(B, kInt4Lens); b += kInt4Warps * 32) {
-        const int n = int4_length(a, b);
-        changed |= n != lens[b];
-        lens[b] = n;
+    for (int b = threadIdx.x; b < min(B, kInt4Lens); b += kInt4Warps * 32) lens[b] = int4_length(a, b);
+    __syncthreads();
+    uint32_t total = 0, rows = 0;
+    for (int b = lane; b < B; b += 32) {
+      const int n = int4_length(a, lens, b);
+      if (n > 0) {
+        total += static_cast<uint32_t>((n + kUnit - 1) / kUnit + 1) * a.Hkv;
+        rows += a.Hkv;
       }
-      if (pass == 1 ? !__syncthreads_or(changed) : (__syncthreads(), B > kInt4Lens)) {
-        if (pass == 1) break;
-        continue;
-      }
-      uint32_t total = 0, rows = 0;
-      for (int b = lane; b < B; b += 32) {
-        const int n = int4_length(a, lens, b);
-        if (n > 0) {
-          total += static_cast<uint32_t>((n + kUnit - 1) / kUnit + 1) * a.Hkv;
-          rows += a.Hkv;
-        }
-      }
+    }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, off);
-        rows += __shfl_xor_sync(0xffffffffu, rows, off);
-      }
-      cut = Int4Cut{total, min(static_cast<uint32_t>(p.ctas), total)};
-      const bool any = blockIdx.x < cut.ctas;
-      cta_begin = any ? cut.begin(blockIdx.x) : 0u;
-      cta_end = any ? cut.begin(blockIdx.x + 1) : 0u;
-      const uint32_t cost = cta_end - cta_begin, each = cost / kInt4Warps, rest = cost % kInt4Warps;
-      const uint32_t lo = cta_begin + each * warp + rest * warp / kInt4Warps;
-      const uint32_t hi = cta_begin + each * (warp + 1) + rest * (warp + 1) / kInt4Warps;
-      mine = 0;
-      if (lo < hi) {
-        // Units before a place: its cost less the rows before it.
-        uint32_t rows_lo, rows_hi = rows;
-        cur = int4_locate<kUnit>(a, lens, B, lane, lo, rows_lo);
-        if (hi < total) int4_locate<kUnit>(a, lens, B, lane, hi, rows_hi);
-        mine = static_cast<int>((hi - rows_hi) - (lo - rows_lo));
-        row_begin = lo - cur.u;
-        if (cur.u == cur.units && mine > 0) {          // the end of a row: begin with the next
-          row_begin += cur.units + 1;
-          --cur.u;
-          int4_advance<kUnit>(a, lens, B, cur);
-        }
-      }
-      if (pass == 0 && !paged && mine > 0 && elect_one()) {
-        for (int i = 0; i < min(min(mine, kInt4Stages), cur.units - cur.u); ++i) {
-          tma_prefetch_l2_4d(&tmK, cur.h, (cur.u + i) * kUnit, cur.b);
-          tma_prefetch_l2_4d(&tmV, cur.h, (cur.u + i) * kUnit, cur.b);
-          tma_prefetch_l2_4d(&tmP, cur.h, (cur.u + i) * kUnit, cur.b);
-        }
+    for (int off = 16; off > 0; off >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, off);
+      rows += __shfl_xor_sync(0xffffffffu, rows, off);
+    }
+    cut = Int4Cut{total, min(static_cast<uint32_t>(p.ctas), total)};
+    if (blockIdx.x < cut.ctas) {
+      cta_begin = cut.begin(blockIdx.x);
+      cta_end = cut.begin(blockIdx.x + 1);
+    }
+    const uint32_t cost = cta_end - cta_begin, each = cost / kInt4Warps, rest = cost % kInt4Warps;
+    const uint32_t lo = cta_begin + each * warp + rest * warp / kInt4Warps;
+    const uint32_t hi = cta_begin + each * (warp + 1) + rest * (warp + 1) / kInt4Warps;
+    if (lo < hi) {
+      // Units before a place: its cost less the rows before it.
+      uint32_t rows_lo, rows_hi = rows;
+      cur = int4_locate<kUnit>(a, lens, B, lane, lo, rows_lo);
+      if (hi < total) int4_locate<kUnit>(a, lens, B, lane, hi, rows_hi);
+      mine = static_cast<int>((hi - rows_hi) - (lo - rows_lo));
+      row_begin = lo - cur.u;
+      if (cur.u == cur.units && mine > 0) {            // the end of a row: begin with the next
+        row_begin += cur.units + 1;
+        --cur.u;
+        int4_advance<kUnit>(a, lens, B, cur);
       }
     }
   }
@@ -567,7 +531,13 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   if (mine > 0) load_q();
 
   // ---- copies, which run over the ends of rows
-  const uint64_t policy = policy_evict_first();
+  // A head-major row's codes are read once and in order.  Token-major ones lie 64
+  // bytes between those of other heads, whose warps want the rest of the line.
+  uint64_t policy;
+  if (p.evict_first)
+    policy = policy_evict_first();
+  else
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
   const int lbs = a.log2_block_size;
   const int pages_per_unit = paged && a.block_size < kUnit ? kUnit >> lbs : 1;
   const int box_rows = kUnit / pages_per_unit;
@@ -744,6 +714,7 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
             const uint32_t e = min((__float_as_uint(vtop[h]) >> 23) + 1u, 253u);
             const float r = __uint_as_float((254u - e) << 23), keep = r / inv_r[h];   // old R / new R
             inv_r[h] = r;
+            if (i == 0) continue;                      // nothing is summed yet
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               eight[nb][2 * h] *= keep;
@@ -857,6 +828,7 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
             const float al = bound[nb][c] == -INFINITY ? 0.f : ex2(ref[nb][c] - now);
             ref[nb][c] = now;
             bound[nb][c] = top[nb][c] + fminf(kRescaleLog2 / scl[nb][c], 3e38f);
+            if (i == 0) continue;
             l_run[nb][c] *= al;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -1043,7 +1015,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   static_assert(kPieces <= 32, "a lane per piece");
   const long long my_row = lane < kPieces ? pieces[lane].row : -1;
   unsigned todo = __ballot_sync(0xffffffffu, my_row >= 0);
-  Int4Shared sh{-1, 0, 0};
   while (todo) {
     const int k0 = __ffs(todo) - 1;
     const long long row = __shfl_sync(0xffffffffu, my_row, k0);
@@ -1052,8 +1023,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     const uint32_t begin = pieces[k0].begin, end = begin + pieces[k0].units;
     const bool whole = begin >= cta_begin && end <= cta_end;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (begin > cta_begin ? 1 : 0);
-    if (!whole && begin >= cta_begin)
-      sh = Int4Shared{row, static_cast<int>(cut.holder(end - 1) - blockIdx.x) + 1, slot};
     constexpr int kChunks = D / 4;
     for (int c = threadIdx.x; c < a.G * kChunks; c += kInt4Warps * 32) {
       const int hd = c / kChunks, d = (c % kChunks) * 4;
@@ -1096,32 +1065,72 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
       }
     }
   }
-  if (gridDim.x > 1 && !p.by_row && threadIdx.x == 0) p.shared[blockIdx.x] = sh;
 }
 
 constexpr int kInt4CombineWarps = 4;
 
 // Merges the partial results of rows that several CTAs share: one warp per (CTA,
-// query head of a group), which takes the row that begins in the CTA's range, its
-// lanes over D.
-template <int D>
+// query head of a group), which takes the row that begins in the CTA's range and
+// goes on beyond, its lanes over D.
+template <int D, int U>
 __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel(const Int4DecodeArgs p) {
-  constexpr int VPL = D / 32, BATCH = 16;
+  constexpr int VPL = D / 32, BATCH = 32;
+  constexpr float kLog2e = 1.4426950408889634074f;
+  __shared__ int lens[kInt4Lens];
   const SplitArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const int w = blockIdx.x * kInt4CombineWarps + (threadIdx.x >> 5);
-  const int cta = w / a.G, head = w - cta * a.G;
+  const uint32_t cta = w / a.G;
+  // The lengths may be read before the wait, as fd_combine_kernel reads them.
+  for (int b = threadIdx.x; b < min(p.B, kInt4Lens); b += kInt4CombineWarps * 32) lens[b] = int4_length(a, b);
+  __syncthreads();
+  uint32_t total = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const int n = int4_length(a, lens, b);
+    if (n > 0) total += static_cast<uint32_t>((n + U - 1) / U + 1) * a.Hkv;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  const Int4Cut cut{total, min(static_cast<uint32_t>(p.ctas), total)};
+  int parts = 0;
+  bool begins = false;                 // with the CTA's range
+  Int4Walk row{};
+  if (cta + 1 < cut.ctas) {
+    uint32_t rows;
+    const uint32_t at = cut.begin(cta + 1), from = cut.begin(cta);
+    row = int4_locate<U>(a, lens, p.B, lane, at, rows);
+    const uint32_t begin = at - row.u;
+    if (row.u > 0 && row.u < row.units && begin >= from) {
+      parts = static_cast<int>(cut.holder(begin + row.units - 1) - cta) + 1;
+      begins = begin == from;
+    }
+  }
   grid_dependency_wait();     // partial results come from the kernel before
   grid_dependents_launch();
-  if (cta >= p.ctas) return;
-  const long long row = __ldcg(&p.shared[cta].row);
-  const int parts = __ldcg(&p.shared[cta].parts), first = __ldcg(&p.shared[cta].first);
-  if (row < 0) return;
-  const size_t r = static_cast<size_t>(row) * a.G + head;
+  if (parts == 0) return;
+  const int head = w - static_cast<int>(cta) * a.G;
+  const size_t r = (static_cast<size_t>(row.b) * a.Hkv + row.h) * a.G + head;
   auto index = [&](int i) {            // of part i
-    return static_cast<size_t>(i == 0 ? first : 2 * (cta + i)) * a.G + head;
+    return static_cast<size_t>(i == 0 && !begins ? 2 * cta + 1 : 2 * (cta + i)) * a.G + head;
   };
-  constexpr float kLog2e = 1.4426950408889634074f;
+  // The first 32 parts are requested at once, with their log-sum-exps.
+  float lb[BATCH], ob[BATCH][VPL];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+      if (s + j < parts) {
+        const size_t x = index(s + j);
+        lb[j] = __ldcg(a.part_lse + x);
+        if constexpr (VPL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + x * D) + lane);
+          ob[j][0] = v.x; ob[j][1] = v.y; ob[j][2] = v.z; ob[j][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + x * D) + lane);
+          ob[j][0] = v.x; ob[j][1] = v.y;
+        }
+      }
+  };
+  load(0);
   float mx = -INFINITY;
   bool nan = false;
   for (int i = lane; i < parts; i += 32) {
@@ -1136,27 +1145,14 @@ __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
   for (int s = 0; s < parts; s += BATCH) {
-    float lb[BATCH], ob[BATCH][VPL];
+    if (s > 0) load(s);
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
       if (s + j < parts) {
-        const size_t x = index(s + j);
-        lb[j] = __ldcg(a.part_lse + x);
-        if constexpr (VPL == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + x * D) + lane);
-          ob[j][0] = v.x; ob[j][1] = v.y; ob[j][2] = v.z; ob[j][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + x * D) + lane);
-          ob[j][0] = v.x; ob[j][1] = v.y;
-        }
-      }
+        const float wt = mx == -INFINITY ? 0.f : ex2((lb[j] - mx) * kLog2e);
+        W += wt;
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-      if (s + j < parts) {
-        const float w = mx == -INFINITY ? 0.f : ex2((lb[j] - mx) * kLog2e);
-        W += w;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) acc[i] += w * ob[j][i];
+        for (int i = 0; i < VPL; ++i) acc[i] += wt * ob[j][i];
       }
   }
   const float inv = W == 0.f ? 0.f : 1.f / W;

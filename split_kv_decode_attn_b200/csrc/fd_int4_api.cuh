@@ -73,9 +73,14 @@ fd_status make_int4_map(CUtensorMap* tm, const void* base, int row_bytes, const 
   const CUtensorMapSwizzle swizzle = row_bytes == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
                                      : row_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                        : CU_TENSOR_MAP_SWIZZLE_NONE;
+  // Fetching 256 bytes at a time pays where a head's rows are neighbours.  Token-
+  // major it fetched other heads' rows (8 x 40,000 tokens in pages of 16: 57.7 us;
+  // 50.2 us without, and without evict-first).
+  const CUtensorMapL2promotion promotion =
+      c.nhd ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides,
                          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FD_OK : FD_ERR_CUDA;
 }
 
@@ -263,19 +268,18 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.scale_log2 = scale * 1.4426950408889634074f;
   a.scale = scale;
   d.B = p->B;
-  // Two partial results per CTA, and what the merge needs to know of it, have to
-  // fit the workspace; more than one CTA per SM would wait for a place.
+  // Two partial results per CTA have to fit the workspace; more than one CTA per
+  // SM would wait for a place.
   int sms = 0;
   if (device_sms(dev, &sms) != FD_OK) return FD_ERR_CUDA;
   const long long rows = static_cast<long long>(p->B) * p->Hkv;
   if (rows * ((p->max_len + unit - 1LL) / unit + 1) > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
   d.by_row = num_splits == 1;
+  d.evict_first = !c.nhd;
   if (!d.by_row) {
-    d.ctas = int4_ctas(sms, rows, a.G, p->D, num_splits);
+    d.ctas = int4_ctas(sms, rows, num_splits);
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = a.part_o + static_cast<size_t>(2) * d.ctas * a.G * p->D;
-    d.shared = reinterpret_cast<fd::Int4Shared*>(static_cast<char*>(workspace) +
-                                                 round256(static_cast<size_t>(2) * d.ctas * a.G * (p->D + 1) * 4));
   }
   const dim3 grid = d.by_row ? dim3(static_cast<unsigned>(p->Hkv), static_cast<unsigned>(p->B))
                              : dim3(static_cast<unsigned>(d.ctas));
@@ -289,8 +293,12 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   if (r == FD_OK && !d.by_row && d.ctas > 1) {
     const dim3 cgrid(static_cast<unsigned>((d.ctas * a.G + fd::kInt4CombineWarps - 1) / fd::kInt4CombineWarps));
     const int threads = fd::kInt4CombineWarps * 32;
-    r = p->D == 128 ? launch_chained(fd::fd_combine_int4_kernel<128>, cgrid, threads, 0, stream, d)
-                    : launch_chained(fd::fd_combine_int4_kernel<64>, cgrid, threads, 0, stream, d);
+    if (p->D == 128)
+      r = unit == 64 ? launch_chained(fd::fd_combine_int4_kernel<128, 64>, cgrid, threads, 0, stream, d)
+                     : launch_chained(fd::fd_combine_int4_kernel<128, 32>, cgrid, threads, 0, stream, d);
+    else
+      r = unit == 64 ? launch_chained(fd::fd_combine_int4_kernel<64, 64>, cgrid, threads, 0, stream, d)
+                     : launch_chained(fd::fd_combine_int4_kernel<64, 32>, cgrid, threads, 0, stream, d);
   }
   return r;
 }

@@ -383,7 +383,8 @@ FD_API fd_status fd_decode_sparse(const fd_problem* p, const void* q, const void
  * over a bf16 cache.
  *   p         the cache (max_blocks_per_seq and max_len are checked, not used,
  *             when it is paged; Hq only as Hq % Hkv)
- *   n_tokens  rows of k_new and v_new, >= 0; 0 launches nothing
+ *   n_tokens  rows of k_new and v_new, >= 0; 0 launches nothing. n_tokens * Hkv
+ *             is below 2^31.
  *   k_new, v_new
  *             bf16, 16-byte aligned: token i, head h starts at element
  *             i * k_stride + h * D (v_stride for V), so that slices of a fused
@@ -401,7 +402,7 @@ FD_API fd_status fd_append_int4(const fd_problem* p, int n_tokens, const void* k
                                 fd_stream_t stream);
 
 /* The rows of a 4-bit cache as a contiguous bf16 cache: s (c - 8) + b, rounded
- * to fp32 and then to bf16. The result is a cache for fd_decode and the entry
+ * once. The result is a cache for fd_decode and the entry
  * points beside it, and what the attention of a prompt reads when it is to see
  * the same K and V as the later steps.
  *   k4, v4, params, seqlens, block_table   as for fd_decode_int4

@@ -62,10 +62,15 @@ def values(packed: np.ndarray, record: np.ndarray):
 
 
 def rounded_values(packed, record) -> np.ndarray:
-    """bf16 bits of what the rows stand for (fp32, then bf16)."""
+    """bf16 bits of what the rows stand for, rounded once: to fp32 with the lowest
+    bit set where that is not exact, and from there to bf16."""
     x, b = values(packed, record)
     with np.errstate(all="ignore"):
-        return _bf16((x + b).astype(np.float32))
+        y = x + b
+        f = y.astype(np.float32)
+        u = f.view(np.uint32)
+        u = u - (np.abs(f.astype(np.float64)) > np.abs(y)) | (f != y)      # towards zero, inexact
+        return _bf16(np.where(np.isfinite(f), u.astype(np.uint32).view(np.float32), f))
 
 
 def attend(q_bits, kc, kr, vc, vr, scale: float):

@@ -45,78 +45,159 @@ struct AppendArgs {
   const __nv_bfloat16* v;
   int64_t k_stride, v_stride;
   const int64_t* slots;      // [n_tokens]
-  int n_tokens;
+  uint32_t n_rows;           // n_tokens Hkv < 2^31
+  uint32_t head_mul;         // x / Hkv = x head_mul >> (31 + head_shift) for x < 2^31
+  int head_shift;
+  int log2_rows;             // rows = 2^log2_rows, or -1
 };
 
-// Quantises the 8 entries that this lane holds of a row; LPG neighbouring
-// lanes hold a group.  Returns the lane's codes, entry i in bits 4i .. 4i+3,
-// and the group's record (scale in the low half, bias in the high half).
+__device__ __forceinline__ uint32_t min2_nan(uint32_t x, uint32_t y) {   // of two bf16
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// The codes of eight entries as defined: clamp(rint((x - b) / s), -8, 7) + 8.
+__device__ __noinline__ uint32_t int4_divided(uint4 raw, float s, float b) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = __fdiv_rn(__fsub_rn((i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]), b), s);
+    codes |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(y), -8.f), 7.f)) + 8) << (4 * i);
+  }
+  return codes;
+}
+
+// Quantises the 16 entries that this lane holds of a row (two words of 8 codes,
+// entry i in bits 4i .. 4i+3); LPG neighbouring lanes hold a group.  Returns the
+// group's record (scale in the low half, bias in the high half).
 //   s = bf16((mx - mn) / 15), b = bf16(mn + 8 s),
 //   c = clamp(rint((x - b) / s), -8, 7) + 8
 // in fp32 (ties to even).  (mx - mn) / 15 is taken as (mx/2 - mn/2) / 7.5 and
 // mn + 8 s with one rounding, so that no bf16 input overflows.  A group with
 // s = 0 gets the code 8; one with a NaN or an infinity gets s = b = NaN.
+//
+// A division per entry made this kernel twice as slow as its copies, so the codes
+// come from two products with reciprocals just below and just above 1 / s
+// (rcp.approx is within 2^-23, they are 2^-22 to either side).  Adding
+// M = 1.5 2^23 + 8 to a product rounds it to an integer, ties to even, in the low
+// bits of the sum.
+//  * Both agree: so does everything between them.
+//  * They differ by one at a tie, Q = d / s = k + 1/2, or next to it.  With x and b
+//    zero or at least 2^-9 s in size, d is a multiple of 2^-17 s and
+//    exact, (k + 1/2) s a multiple of 2^-9 s, and |Q| < 9 puts the two products
+//    within 9 (2^-22 + 2^-23 + 2^-24) < 2^-17 of Q: then it is a tie.  The sum of
+//    the two results is odd, twice the tie, and beyond 2^24, where fp32 holds only
+//    even numbers: the addition itself rounds half to even.  It is exact when they
+//    agree, so it is used for all entries.
+//    (A smaller entry, |x| < 2^-9 s, comes next to a tie only when -b / s does,
+//    within 2^-9 + 2^-17: looking at b saves a look at every entry, 8 us of 34.)
+//  * Otherwise (b of that kind, a bias so large that codes have to be clamped, a
+//    scale whose reciprocal overflows) the lane divides.
 template <int LPG>
-__device__ __forceinline__ uint32_t int4_quantise(uint4 raw, uint32_t& record) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-  float mn = INFINITY, mx = -INFINITY;
-  uint32_t top = 0;
+__device__ __forceinline__ uint32_t int4_quantise(const uint4 (&raw)[2], uint32_t (&codes)[2]) {
+  const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+  uint32_t lo2 = w[0], hi2 = w[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-    mn = fminf(mn, fminf(x[2 * i], x[2 * i + 1]));
-    mx = fmaxf(mx, fmaxf(x[2 * i], x[2 * i + 1]));
-    top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  for (int i = 1; i < 8; ++i) {
+    lo2 = min2_nan(lo2, w[i]);
+    hi2 = max2_nan(hi2, w[i]);
   }
+  // The smallest entry and minus the largest: one minimum for both.
+  uint32_t ends = min2_nan(__byte_perm(lo2, hi2 ^ 0x80008000u, 0x5410), __byte_perm(lo2, hi2 ^ 0x80008000u, 0x7632));
 #pragma unroll
-  for (int off = 1; off < LPG; off <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-  }
+  for (int off = 1; off < LPG; off <<= 1) ends = min2_nan(ends, __shfl_xor_sync(0xffffffffu, ends, off));
+  const float mn = bf16_lo(ends), mx = -bf16_hi(ends);
   const float half_range = __fsub_rn(__fmul_rn(mx, 0.5f), __fmul_rn(mn, 0.5f));
-  const float s = round_to_bf16(__fdiv_rn(half_range, 7.5f));
+  codes[0] = codes[1] = 0x88888888u;
+  if (!(half_range < INFINITY)) return 0x7fc07fc0u;
+  // half_range / 7.5: the product with the reciprocal and one correction by its
+  // exact residue (Markstein 1990; right for all 2^23 significands), or the
+  // division where the residue could underflow.
+  constexpr float kInv = 1.f / 7.5f;
+  float q = __fmul_rn(half_range, kInv);
+  q = __fmaf_rn(__fmaf_rn(-q, 7.5f, half_range), kInv, q);
+  if (half_range < 0x1p-90f) q = __fdiv_rn(half_range, 7.5f);
+  const float s = round_to_bf16(q);
   const float b = round_to_bf16(__fmaf_rn(8.f, s, mn));
-  const bool finite = top < 0x7f80u;
-  record = finite ? pack_bf16x2(s, b) : 0x7fc07fc0u;
-  if (!finite || !(s > 0.f)) return 0x88888888u;
-  uint32_t codes = 0;
+  const uint32_t record = pack_bf16x2(s, b);
+  if (!(s > 0.f)) return record;
+
+  constexpr float kM = 12582920.f;                     // 1.5 2^23 + 8
+  constexpr uint32_t kBase = 0x4bc00000u * 0x11111111u;   // 2 kM - 16, in every code's place
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float below = __fmul_rn(r, 1.f - 0x1p-22f), above = __fmul_rn(r, 1.f + 0x1p-22f);
+  auto entry = [&](int i) { return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); };
+  uint32_t differ = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = rintf(__fdiv_rn(__fsub_rn(x[i], b), s));
-    codes |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(y, -8.f), 7.f)) + 8) << (4 * i);
+  for (int x = 0; x < 2; ++x) {
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      const float d = __fsub_rn(entry(8 * x + i), b);
+      const float t0 = __fmaf_rn(d, below, kM), t1 = __fmaf_rn(d, above, kM);
+      differ |= __float_as_uint(t0) ^ __float_as_uint(t1);
+      c = c * 16u + __float_as_uint(__fadd_rn(t0, t1));
+    }
+    codes[x] = c - kBase;
   }
-  return codes;
+  const float y0 = __fmul_rn(__fsub_rn(mn, b), above), y1 = __fmul_rn(__fsub_rn(mx, b), above);
+  bool divide = y0 < -8.25f || y1 > 7.25f || s < 0x1p-100f;
+  if (differ) {
+    const float y = __fmul_rn(b, r), off = fabsf(y - rintf(y));
+    divide |= off > 0.5f - 0x1p-8f || (b != 0.f && fabsf(b) < s * 0x1p-9f);
+  }
+  if (divide) {
+    codes[0] = int4_divided(raw[0], s, b);
+    codes[1] = int4_divided(raw[1], s, b);
+  }
+  return record;
 }
 
-// D / 8 lanes per row; the rows of a token are its K heads, then its V heads.
+// D / 16 lanes take the K and the V row of one (token, KV head), so that the
+// record leaves as one 16-byte store; rows of whole warps of lanes need neither
+// shared memory nor a barrier.  26,313 tokens of 8 heads (D = 128, 138 MB): 28 us,
+// 4.9 TB/s, bound by instruction issue (12 per entry; 24 us without the rules for
+// ties).  With a division per entry and 64-bit divisions for the addresses it took
+// about 50 us.
 template <int D>
 __global__ void __launch_bounds__(256) fd_append_int4_kernel(const AppendArgs a) {
+  constexpr int LPR = D / 16, LPG = LPR / 2;
+  const uint32_t at = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const int part = threadIdx.x % LPR;
+  const uint32_t unit = min(at, a.n_rows - 1);         // whole warps take part in the shuffles
+  const uint32_t token = static_cast<uint32_t>((static_cast<uint64_t>(unit) * a.head_mul) >> (31 + a.head_shift));
+  const int head = static_cast<int>(unit - token * a.c.Hkv);
+  const uint4* k = reinterpret_cast<const uint4*>(a.k + token * a.k_stride + head * D) + 2 * part;
+  const uint4* v = reinterpret_cast<const uint4*>(a.v + token * a.v_stride + head * D) + 2 * part;
   grid_dependency_wait();
   grid_dependents_launch();
-  constexpr int LPR = D / 8;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
-  const int part = threadIdx.x % LPR;
-  const int64_t n_rows = static_cast<int64_t>(a.n_tokens) * 2 * a.c.Hkv;
-  const int64_t row = at < n_rows ? at : n_rows - 1;      // whole warps take part in the shuffles
-  const int token = static_cast<int>(row / (2 * a.c.Hkv));
-  const int unit = static_cast<int>(row - static_cast<int64_t>(token) * 2 * a.c.Hkv);
-  const bool is_v = unit >= a.c.Hkv;
-  const int head = is_v ? unit - a.c.Hkv : unit;
-  const __nv_bfloat16* src = is_v ? a.v + token * a.v_stride : a.k + token * a.k_stride;
-  const uint4 raw = *reinterpret_cast<const uint4*>(src + head * D + part * 8);
-  uint32_t record;
-  const uint32_t codes = int4_quantise<LPR / 2>(raw, record);
-  const int64_t slot = a.slots[token];
-  if (at >= n_rows || slot < 0 || slot >= static_cast<int64_t>(a.c.planes) * a.c.rows) return;
-  const int plane = static_cast<int>(slot / a.c.rows);
-  const size_t to = int4_row(a.c, plane, head, static_cast<int>(slot - static_cast<int64_t>(plane) * a.c.rows));
-  uint8_t* dst = is_v ? a.c.v4 : a.c.k4;
-  *reinterpret_cast<uint32_t*>(dst + to * (D / 2) + part * 4) = codes;
-  if (part % (LPR / 2) == 0)
-    *reinterpret_cast<uint32_t*>(a.c.params + to * 16 + (is_v ? 8 : 0) + (part / (LPR / 2)) * 4) = record;
+  const uint4 kr[2] = {__ldcs(k), __ldcs(k + 1)}, vr[2] = {__ldcs(v), __ldcs(v + 1)};
+  const int64_t slot = __ldcg(a.slots + token);
+  uint32_t kc[2], vc[2];
+  const uint32_t krec = int4_quantise<LPG>(kr, kc), vrec = int4_quantise<LPG>(vr, vc);
+  const uint32_t krec1 = __shfl_down_sync(0xffffffffu, krec, LPG), vrec1 = __shfl_down_sync(0xffffffffu, vrec, LPG);
+  const uint64_t s = static_cast<uint64_t>(slot);
+  if (at >= a.n_rows || s >= static_cast<uint64_t>(a.c.planes) * a.c.rows) return;
+  size_t to;
+  if (a.c.nhd) {
+    to = s * a.c.Hkv + head;
+  } else {
+    const uint32_t plane = a.log2_rows >= 0 ? static_cast<uint32_t>(s >> a.log2_rows)
+                           : s >> 32        ? static_cast<uint32_t>(s / static_cast<uint32_t>(a.c.rows))
+                                            : static_cast<uint32_t>(s) / static_cast<uint32_t>(a.c.rows);
+    to = s + (static_cast<size_t>(plane) * (a.c.Hkv - 1) + head) * a.c.rows;
+  }
+  reinterpret_cast<uint2*>(a.c.k4 + to * (D / 2))[part] = make_uint2(kc[0], kc[1]);
+  reinterpret_cast<uint2*>(a.c.v4 + to * (D / 2))[part] = make_uint2(vc[0], vc[1]);
+  if (part == 0) reinterpret_cast<uint4*>(a.c.params)[to] = make_uint4(krec, krec1, vrec, vrec1);
 }
 
 // ---------------------------------------------------------------- expand
@@ -131,50 +212,69 @@ struct ExpandArgs {
   __nv_bfloat16* v;
 };
 
-// The 8 codes of a word as the bf16 values they stand for.
+// The 8 codes of a word as the bf16 values they stand for.  128 + c is a bf16
+// number with c in its low bits; taking 136 off is exact, and the fused multiply-
+// add rounds s (c - 8) + b once.
 __device__ __forceinline__ uint4 int4_values(uint32_t codes, uint32_t record) {
-  const float s = bf16_lo(record), b = bf16_hi(record);
-  uint32_t w[4];
+  const uint32_t s = __byte_perm(record, record, 0x1010), b = __byte_perm(record, record, 0x3232);
+  uint32_t v[4];                                       // entries i and i + 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c0 = static_cast<int>((codes >> (8 * i)) & 15u) - 8;
-    const int c1 = static_cast<int>((codes >> (8 * i + 4)) & 15u) - 8;
-    w[i] = pack_bf16x2(__fmaf_rn(s, static_cast<float>(c0), b), __fmaf_rn(s, static_cast<float>(c1), b));
+    const uint32_t c = ((codes >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(c), "r"(0x43084308u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(s), "r"(v[i]), "r"(b));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
-constexpr int kExpandTokens = 32;
+constexpr int kExpandTokens = 64;
 
-// One CTA per 32 tokens of one KV head of one sequence; D / 8 lanes per row.
+// One CTA per 64 tokens of one KV head of one sequence; D / 8 lanes per row, and
+// a thread's rows are all requested before the first is used.  26,313 tokens of 8
+// heads (D = 128, 138 MB): 22 us, 6.3 TB/s, bound by HBM.  (32 tokens per CTA 25.6
+// us, 128 26.7 against 25.4 at 64, all with plain stores; the streaming stores gave
+// the rest, as the output leaves the small input in L2 alone.  With conversions
+// from integers and a multiply-add per entry in fp32 it took about 50 us.)
 template <int D>
 __global__ void __launch_bounds__(256) fd_expand_int4_kernel(const ExpandArgs a) {
   grid_dependency_wait();
   grid_dependents_launch();
-  constexpr int LPR = D / 8;
+  constexpr int LPR = D / 8, STEP = 256 / LPR, N = kExpandTokens / STEP;
   const int b = blockIdx.z, head = blockIdx.y;
   const int n = seq_length(a.seqlens, b, a.max_len);
-  const int t0 = blockIdx.x * kExpandTokens;
+  const int t0 = blockIdx.x * kExpandTokens + threadIdx.x / LPR;
   const int part = threadIdx.x % LPR;
-  for (int t = t0 + threadIdx.x / LPR; t < min(n, t0 + kExpandTokens); t += 256 / LPR) {
-    int plane = b, row = t;
-    if (a.block_table) {
-      plane = a.block_table[static_cast<size_t>(b) * a.max_blocks + (t >> a.log2_block_size)];
-      row = t & ((1 << a.log2_block_size) - 1);
+  if (t0 >= n) return;
+  int plane[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    plane[i] = b;
+    if (a.block_table)
+      plane[i] = t0 + i * STEP < n ? __ldcg(a.block_table + static_cast<size_t>(b) * a.max_blocks + ((t0 + i * STEP) >> a.log2_block_size)) : -1;
+  }
+  uint32_t kc[N], vc[N], kr[N], vr[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = t0 + i * STEP;
+    kc[i] = vc[i] = kr[i] = vr[i] = 0;                 // a page outside the pool: zeros
+    if (t < n && plane[i] >= 0 && plane[i] < a.c.planes) {
+      const size_t from = int4_row(a.c, plane[i], head, a.block_table ? t & (a.c.rows - 1) : t);
+      const uint32_t* rec = reinterpret_cast<const uint32_t*>(a.c.params + from * 16) + part / (LPR / 2);
+      kc[i] = reinterpret_cast<const uint32_t*>(a.c.k4 + from * (D / 2))[part];
+      vc[i] = reinterpret_cast<const uint32_t*>(a.c.v4 + from * (D / 2))[part];
+      kr[i] = rec[0];
+      vr[i] = rec[2];
     }
-    uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-    if (plane >= 0 && plane < a.c.planes) {
-      const size_t from = int4_row(a.c, plane, head, row);
-      const uint8_t* rec = a.c.params + from * 16 + (part / (LPR / 2)) * 4;
-      kv = int4_values(*reinterpret_cast<const uint32_t*>(a.c.k4 + from * (D / 2) + part * 4),
-                       *reinterpret_cast<const uint32_t*>(rec));
-      vv = int4_values(*reinterpret_cast<const uint32_t*>(a.c.v4 + from * (D / 2) + part * 4),
-                       *reinterpret_cast<const uint32_t*>(rec + 8));
-    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int t = t0 + i * STEP;
+    if (t >= n) break;
     const size_t to = a.c.nhd ? (static_cast<size_t>(b) * a.max_len + t) * a.c.Hkv + head
                               : (static_cast<size_t>(b) * a.c.Hkv + head) * a.max_len + t;
-    *reinterpret_cast<uint4*>(a.k + to * D + part * 8) = kv;
-    *reinterpret_cast<uint4*>(a.v + to * D + part * 8) = vv;
+    __stcs(reinterpret_cast<uint4*>(a.k + to * D) + part, int4_values(kc[i], kr[i]));
+    __stcs(reinterpret_cast<uint4*>(a.v + to * D) + part, int4_values(vc[i], vr[i]));
   }
 }
 

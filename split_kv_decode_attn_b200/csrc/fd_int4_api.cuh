@@ -5,8 +5,7 @@
 
 namespace {
 
-// The cache that p describes, checked: FD_KV_INT4, paged exactly when
-// block_table is given (paged caches that need no table pass any_table).
+// The cache that p describes, checked.
 fd_status int4_cache(const fd_problem* p, const void* k4, const void* v4, const void* params,
                      fd::Int4Cache* c) {
   if (!p || !k4 || !v4 || !params) return FD_ERR_INVALID_ARGUMENT;
@@ -182,6 +181,8 @@ fd_status fd_append_int4(const fd_problem* p, int n_tokens, const void* k_new, i
   const int64_t row = static_cast<int64_t>(p->Hkv) * p->D;
   if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < row || v_stride < row)
     return FD_ERR_INVALID_ARGUMENT;
+  const long long rows = static_cast<long long>(n_tokens) * p->Hkv;
+  if (rows > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
   if (n_tokens == 0 || a.c.rows == 0) return FD_OK;
   int dev = 0;
   const fd_status arch = this_device(&dev);
@@ -191,12 +192,12 @@ fd_status fd_append_int4(const fd_problem* p, int n_tokens, const void* k_new, i
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.slots = slots;
-  a.n_tokens = n_tokens;
-  const long long rows = static_cast<long long>(n_tokens) * 2 * p->Hkv;
-  const long long per = 256 / (p->D / 8);
-  const long long grid = (rows + per - 1) / per;
-  if (grid > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
-  const dim3 g(static_cast<unsigned>(grid));
+  a.n_rows = static_cast<uint32_t>(rows);
+  while ((1 << a.head_shift) < p->Hkv) ++a.head_shift;     // Granlund and Montgomery's division
+  a.head_mul = static_cast<uint32_t>(((1ull << (31 + a.head_shift)) + p->Hkv - 1) / p->Hkv);
+  a.log2_rows = p->block_size ? ilog2(p->block_size) : -1;
+  const long long per = 256 / (p->D / 16);
+  const dim3 g(static_cast<unsigned>((rows + per - 1) / per));
   return p->D == 128 ? launch_chained(fd::fd_append_int4_kernel<128>, g, 256, 0, stream, a)
                      : launch_chained(fd::fd_append_int4_kernel<64>, g, 256, 0, stream, a);
 }

@@ -87,6 +87,42 @@ def test_append_of_special_and_tied_rows():
         assert np.array_equal(np.where(zero, half & 0x7FFF, half), np.where(zero, rec & 0x7FFF, rec))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_next_to_ties(D):
+    """Entries that lie on, and a bit off, the border between two codes: integer
+    groups of range 15 (scale 1) and 30 (scale 2), entries of all sizes down to
+    the smallest beside them, biases up to where codes have to be clamped."""
+    n = 2048
+    r = np.random.default_rng(D)
+    x = np.empty((n, D))
+    for i in range(n):
+        size = 2.0 ** r.integers(-130, 100)
+        kind = i % 4
+        if kind == 0:      # borders exactly, and tiny entries
+            row = r.integers(-15, 16, D) * 0.5
+            tiny = r.random(D) < 0.3
+            row[tiny] = r.choice([-1, 1], tiny.sum()) * 2.0 ** -r.integers(1, 40, tiny.sum())
+            row[::D // 2], row[1::D // 2] = -7.5, 7.5
+        elif kind == 1:    # a narrow band around the borders
+            row = (r.integers(-15, 16, D) * 0.5) * (1 + r.integers(-2, 3, D) / 128)
+        elif kind == 2:    # an offset that bf16 holds coarsely
+            row = 2.0 ** r.integers(0, 9) + r.integers(-8, 8, D) * 0.25
+        else:
+            row = r.standard_normal(D) * 2.0 ** r.integers(-20, 1, D)
+        x[i] = row * size
+    x = wl.f64_to_bf16_bits(x).reshape(n, 1, D)
+    k4 = torch().zeros((1, 1, n, D // 2), dtype=torch().uint8, device="cuda")
+    v4, prm = torch().zeros_like(k4), up(np.zeros((1, 1, n, 8), np.uint16))
+    fd.append_int4(up(x), up(x[::-1].copy()), up(np.arange(n)), k4, v4, prm)
+    c, rec = int4.quantise(x[:, 0])
+    assert np.array_equal(k4[0, 0].cpu().numpy(), int4.pack(c))
+    assert np.array_equal(v4[0, 0].cpu().numpy(), int4.pack(c[::-1]))
+    # the sign of a zero is free
+    assert np.array_equal(rec & 0x7FFF, bits(prm)[0, 0, :, :4] & 0x7FFF)
+    nonzero = (rec & 0x7FFF) != 0
+    assert np.array_equal(rec[nonzero], bits(prm)[0, 0, :, :4][nonzero])
+
+
 # ------------------------------------------------------------------- expand
 
 @pytest.mark.parametrize("D", [64, 128])

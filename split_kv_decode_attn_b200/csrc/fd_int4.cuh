@@ -302,11 +302,30 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
       : "memory");
 }
 
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <class T>
@@ -432,6 +451,17 @@ struct Int4Piece {
 };
 static_assert(sizeof(Int4Piece) == 16, "as laid out in shared memory");
 
+// What a warp has to copy: `units` units from where the walk stands.
+struct Int4Range {
+  Int4Walk from;
+  int units;
+};
+static_assert(sizeof(Int4Range) <= 32, "as laid out in shared memory");
+
+// Registers per thread: 4 copying warps and 8 computing ones share what the CTA
+// starts with, 384 x 168 (the host checks that the kernel was built with these).
+constexpr int kInt4CopyWarps = 4, kInt4StartRegs = 168, kInt4CopyRegs = 40, kInt4ComputeRegs = 232;
+
 template <int D, int NB, class SH>
 struct Int4Smem {
   static constexpr int kUnit = SH::UNIT, kInt4Warps = SH::WARPS, kInt4Stages = SH::STAGES;
@@ -458,8 +488,10 @@ struct Int4Smem {
   static constexpr int kFirstOffset = kVRecOffset + kInt4Warps * kVRecBytes;
   static constexpr int kRowOffset = kFirstOffset + kInt4Warps * kStateFloats * 4;   // Int4Piece[2 warps]
   static constexpr int kLenOffset = kRowOffset + 2 * kInt4Warps * 16;
-  static constexpr int kBarOffset = kLenOffset + 4 * kInt4Lens;
-  static constexpr int kErrorOffset = kBarOffset + 8 * kInt4Warps * kInt4Stages;
+  static constexpr int kRangeOffset = kLenOffset + 4 * kInt4Lens;             // Int4Range[warps]
+  static constexpr int kBarOffset = kRangeOffset + 32 * kInt4Warps;   // filled, then free, [warps][stages]
+  static constexpr int kFreeBars = 8 * kInt4Warps * kInt4Stages;
+  static constexpr int kErrorOffset = kBarOffset + 2 * kFreeBars;
   static constexpr int kDynamicBytes = kErrorOffset + 16 + 1024;   // room to align to 1 KB
   static_assert(kDynamicBytes <= 227 * 1024, "shared memory per CTA");
 };
@@ -483,6 +515,96 @@ template <int D>
 __device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
   const uint32_t a = r * (D / 2) + col;
   return D == 128 ? a ^ ((r << 3) & 0x30u) : a ^ ((r << 2) & 0x10u);
+}
+
+// The copying warps.  Each fills the rings of two computing warps, one per half of
+// its lanes, running ahead over the ends of rows: a warp that issued its own copies
+// spent 450 cycles of a unit's 3,650 on it, and 950 of 4,200 with two pages per
+// unit.
+template <int D, class SH, class L>
+__device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CUtensorMap* tmK,
+                                               const CUtensorMap* tmV, const CUtensorMap* tmP,
+                                               uint8_t* smem, const Int4Range* ranges, const int* lens,
+                                               int copy_warp, int lane) {
+  constexpr int kUnit = SH::UNIT, kStages = SH::STAGES;
+  constexpr int kHalf = 32 * kInt4CopyWarps / SH::WARPS;   // lanes per ring
+  static_assert(kHalf == 16 && kUnit / 8 <= kHalf, "a lane per page of a unit");
+  set_regs_down<kInt4CopyRegs>();
+  const SplitArgs& a = p.a;
+  const int lbs = a.log2_block_size;
+  const bool paged = a.block_size != 0;
+  const int pages_per_unit = paged && a.block_size < kUnit ? kUnit >> lbs : 1;
+  const int box_rows = kUnit / pages_per_unit;
+  // A head-major row's codes are read once and in order.  Token-major ones lie 64
+  // bytes between those of other heads, whose warps want the rest of the line.
+  uint64_t policy;
+  if (p.evict_first)
+    policy = policy_evict_first();
+  else
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+  const int sub = lane & (kHalf - 1), of = 2 * copy_warp + (lane >> 4);
+  const uint32_t ring = smem_u32(smem) + of * L::kWarpBytes;
+  const uint32_t bar = smem_u32(smem) + L::kBarOffset + 8 * kStages * of;
+  bar_sync(1, (SH::WARPS + kInt4CopyWarps) * 32);
+  Int4Walk at = ranges[of].from;
+  const int units = ranges[of].units;
+  // The page of this lane's box in the next unit (lanes past the boxes: none).
+  auto page_at = [&]() {
+    const int pg = ((at.u * kUnit) >> lbs) + sub;
+    return paged && sub < pages_per_unit && pg < ((at.n + a.block_size - 1) >> lbs)
+               ? __ldcg(a.block_table + static_cast<size_t>(at.b) * a.max_blocks_per_seq + pg)
+               : 0;
+  };
+  int issued = 0, stage = 0;
+  uint32_t phase = 1;                  // a fresh barrier counts as passed in this phase
+  int page = units > 0 ? page_at() : at.b;
+  uint64_t since = 0;
+  bool failed = false;
+  while (__any_sync(0xffffffffu, issued < units && !failed)) {
+    const bool more = issued < units && !failed;
+    const uint32_t full = bar + 8 * stage;
+    const bool ready = more && mbar_test(full + L::kFreeBars, phase);
+    if (ready) {
+      const int t0 = at.u * kUnit;
+      const uint32_t st = ring + stage * L::kStageBytes;
+      const int boxes = paged ? min(pages_per_unit, ((at.n + a.block_size - 1) >> lbs) - (t0 >> lbs)) : 1;
+      const int row = paged ? t0 & (a.block_size - 1) : t0;
+      const int plane = paged ? page : at.b;
+      if (sub == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (D + 16));
+      __syncwarp(0xffffu << (lane & 16));
+      if (sub < boxes) {
+        const uint32_t r = sub * box_rows;
+        tma_load_4d(st + r * L::kRowBytes, tmK, full, at.h, row, plane, policy);
+        tma_load_4d(st + L::kV + r * L::kRowBytes, tmV, full, at.h, row, plane, policy);
+        tma_load_4d(st + L::kP + r * 16, tmP, full, at.h, row, plane, policy);
+      }
+      if (++issued < units) {
+        int4_advance<kUnit>(a, lens, p.B, at);
+        page = page_at();
+      }
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      since = 0;
+    } else if (more) {
+      const uint64_t now = global_timer_ns();
+      if (since == 0) since = now;
+      failed = now - since > kWaitLimitNs;
+    }
+    __syncwarp();
+  }
+  volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);
+  if (failed && sub == 0) {
+    raise_device_error(1u);
+    *cta_error = 1;
+  }
+  __syncthreads();
+  if (!*cta_error || sub != 0) return;
+  // After an error copies may be under way that no warp waits for, the last in
+  // each stage; none may land when the CTA has gone.
+  for (int i = max(issued - kStages, 0); i < issued; ++i)
+    if (!mbar_wait(bar + 8 * (i % kStages), (i / kStages) & 1, kWaitLimitNs)) raise_device_error(2u);
 }
 
 // Decode attention over a 4-bit cache.  A row that lies within a warp's range is
@@ -514,7 +636,7 @@ __device__ __forceinline__ uint32_t int4_code_offset(uint32_t r, uint32_t col) {
 // unit in place of shuffles), and the weights are 2^7 p, so that they use f16's
 // range: up to 2^15, and down to 2^-31 of the largest before one is lost.
 template <int D, int NB, class SH>
-__global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
+__global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     fd_split_int4_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmP, const Int4DecodeArgs p) {
@@ -539,8 +661,15 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   const int B = p.B;
   const bool paged = a.block_size != 0;
 
-  if (lane == 0) {
-    for (int s = 0; s < kInt4Stages; ++s) mbar_init(bar + 8 * s, 1);
+  static_assert(SH::CTAS == 1 && kInt4Warps == 8 &&
+                    (kInt4Warps + kInt4CopyWarps) * kInt4StartRegs ==
+                        kInt4Warps * kInt4ComputeRegs + kInt4CopyWarps * kInt4CopyRegs,
+                "the warps' shares are what the CTA starts with");
+  if (lane == 0 && warp < kInt4Warps) {
+    for (int s = 0; s < kInt4Stages; ++s) {
+      mbar_init(bar + 8 * s, 1);
+      mbar_init(bar + L::kFreeBars + 8 * s, 1);
+    }
     fence_mbar_init();
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
@@ -563,6 +692,17 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   uint32_t cta_begin = 0, cta_end = 0;
   uint32_t row_begin = 0;              // where cur's row begins
   int mine = 0;
+  if (!p.by_row) {
+    for (int b = threadIdx.x; b < min(B, kInt4Lens); b += (kInt4Warps + kInt4CopyWarps) * 32)
+      lens[b] = int4_length(a, b);
+    __syncthreads();
+  }
+  Int4Range* ranges = reinterpret_cast<Int4Range*>(smem + L::kRangeOffset);
+  if (warp >= kInt4Warps) {
+    int4_copy_warp<D, SH, L>(p, &tmK, &tmV, &tmP, smem, ranges, lens, warp - kInt4Warps, lane);
+    return;
+  }
+
   if (p.by_row) {
     cur.b = blockIdx.y;
     cur.h = blockIdx.x;
@@ -572,8 +712,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     cur.u = cur.units * warp / kInt4Warps;
     mine = cur.units * (warp + 1) / kInt4Warps - cur.u;
   } else {
-    for (int b = threadIdx.x; b < min(B, kInt4Lens); b += kInt4Warps * 32) lens[b] = int4_length(a, b);
-    __syncthreads();
     uint32_t total = 0, rows = 0;
     for (int b = lane; b < B; b += 32) {
       const int n = int4_length(a, lens, b);
@@ -610,8 +748,12 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     }
   }
 
-  // q's loads go ahead of the copies (behind them they took 2 us more to come
-  // back): word w of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
+  if (lane == 0) ranges[warp] = Int4Range{cur, mine};
+  __syncwarp();
+  bar_arrive(1, (kInt4Warps + kInt4CopyWarps) * 32);    // to the copying warps
+  set_regs_up<kInt4ComputeRegs>();
+
+  // Word w of q of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
   uint4 raw[NB][2][KW];
   auto load_q = [&]() {
 #pragma unroll
@@ -629,57 +771,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
     }
   };
   if (mine > 0) load_q();
-
-  // ---- copies, which run over the ends of rows
-  // A head-major row's codes are read once and in order.  Token-major ones lie 64
-  // bytes between those of other heads, whose warps want the rest of the line.
-  uint64_t policy;
-  if (p.evict_first)
-    policy = policy_evict_first();
-  else
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-  const int lbs = a.log2_block_size;
-  const int pages_per_unit = paged && a.block_size < kUnit ? kUnit >> lbs : 1;
-  const int box_rows = kUnit / pages_per_unit;
-  Int4Walk ahead = cur;                                // the unit to be copied next
-  // The page of this lane's box in that unit (lanes past the boxes: none).
-  auto page_ahead = [&]() {
-    const int pg = ((ahead.u * kUnit) >> lbs) + lane;
-    return paged && lane < pages_per_unit && pg < ((ahead.n + a.block_size - 1) >> lbs)
-               ? __ldg(a.block_table + static_cast<size_t>(ahead.b) * a.max_blocks_per_seq + pg)
-               : 0;
-  };
-  int issued = 0;
-  int next_page = mine > 0 ? page_ahead() : 0;
-  auto issue = [&](uint32_t s) {                       // into stage s
-    const int t0 = ahead.u * kUnit;
-    const uint32_t st = ring_at + s * L::kStageBytes;
-    const uint32_t full = bar + 8 * s;
-    if (!paged) {
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full, kUnit * (D + 16));
-        tma_load_4d(st, &tmK, full, ahead.h, t0, ahead.b, policy);
-        tma_load_4d(st + L::kV, &tmV, full, ahead.h, t0, ahead.b, policy);
-        tma_load_4d(st + L::kP, &tmP, full, ahead.h, t0, ahead.b, policy);
-      }
-    } else {
-      const int boxes = min(pages_per_unit, ((ahead.n + a.block_size - 1) >> lbs) - (t0 >> lbs));
-      if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (D + 16));
-      __syncwarp();
-      if (lane < boxes) {
-        const int row = t0 & (a.block_size - 1);
-        const uint32_t r = lane * box_rows;
-        tma_load_4d(st + r * L::kRowBytes, &tmK, full, ahead.h, row, next_page, policy);
-        tma_load_4d(st + L::kV + r * L::kRowBytes, &tmV, full, ahead.h, row, next_page, policy);
-        tma_load_4d(st + L::kP + r * 16, &tmP, full, ahead.h, row, next_page, policy);
-      }
-    }
-    if (++issued < mine) {
-      int4_advance<kUnit>(a, lens, B, ahead);
-      next_page = page_ahead();
-    }
-  };
-  while (issued < min(mine, kInt4Stages)) issue(issued);
 
   // Offsets within a unit of this lane's loads: codes of K (slot g), of V
   // (slots 2 t4 and 2 t4 + 1) and the records of slot g.
@@ -1003,10 +1094,10 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
         for (int nb = 0; nb < NB; ++nb) mma_f16_16816(eight[nb], v8, pb[nb][h][0], pb[nb][h][1]);
       }
     }
-    // The stage is read (and its records were written to): refill it.
+    // The stage is read (and its records were written to): it may be refilled.
     fence_proxy_async_smem();
     __syncwarp();
-    if (issued < mine) issue(stage);
+    if (lane == 0) mbar_arrive(bar + L::kFreeBars + 8 * stage);
     if (++stage == kInt4Stages) {
       stage = 0;
       phase ^= 1;
@@ -1085,15 +1176,6 @@ __global__ void __launch_bounds__(SH::WARPS * 32, SH::CTAS)
   if (failed && lane == 0) {
     raise_device_error(1u);
     *cta_error = 1;
-    // No copy may still be landing in shared memory when the CTA retires: the
-    // copies in flight are the last ones issued, in the stages from `stage` on.
-    for (int i = 0; i < kInt4Stages; ++i) {
-      if (!mbar_wait(bar + 8 * stage, phase, kWaitLimitNs)) raise_device_error(2u);
-      if (++stage == kInt4Stages) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
   }
   // Sequences without a token belong to no range.
   if (!p.by_row || cta_end == 0) {

@@ -119,12 +119,16 @@ fd_status launch_split_int4(const Int4Maps& m, const fd::Int4DecodeArgs& a, dim3
   static std::atomic<unsigned long long> attr_ctx[kMaxDevices];   // as launch_split's
   const unsigned long long ctx = current_context_id();
   if (ctx == 0 || attr_ctx[dev].load() != ctx) {
+    // The warps' shares of the registers have to be there when it starts.
+    cudaFuncAttributes built;
+    if (cudaFuncGetAttributes(&built, kern) != cudaSuccess || built.numRegs < fd::kInt4StartRegs)
+      return FD_ERR_CUDA;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              L::kDynamicBytes) != cudaSuccess)
       return FD_ERR_CUDA;
     attr_ctx[dev].store(ctx);
   }
-  return launch_chained(kern, grid, SH::WARPS * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
+  return launch_chained(kern, grid, (SH::WARPS + fd::kInt4CopyWarps) * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
 }
 
 // Do two arrays of int32 share memory?

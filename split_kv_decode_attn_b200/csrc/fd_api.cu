@@ -726,13 +726,26 @@ int int4_ctas(int num_sms, long long rows, int num_splits) {
   return static_cast<int>(std::clamp<long long>(rows * num_splits / 2, 1, num_sms));
 }
 
-// The split count to ask for over a 4-bit cache: the least that fills the SMs.
-// One CTA per row, with no merge, is left for batches of at most one row per SM
-// whose histories hold no more than a unit of 64 tokens for each of a CTA's
-// eight warps.
-int plan_int4(int num_sms, long long rows, int longest) {
+// Deal eight KV heads at a time?  Their rows are neighbours in a token-major cache,
+// and warps need no merge; but every CTA leaves sixteen partial results, which the
+// workspace has to hold and the merge to read, up to 30 per row of the batch's five
+// (measured, token-major: 5 x 20,000 tokens at 64/8 heads 40.9 -> 35.4 us, 8 x up to
+// 40,000 at 32/8 49 -> 42; below, 4 x 65,536 70.5 -> 72.0 and 2 x 65,536 42.8 -> 44.4.
+// Head-major: 32 x up to 8,192 43.5 -> 41.6, 5 x 20,000 33.9 -> 34.2).
+bool int4_heads(int num_sms, int B, int Hkv, int num_splits) {
+  return Hkv % 8 == 0 && static_cast<long long>(B) * Hkv >= 40 &&
+         static_cast<long long>(B) * Hkv * num_splits >= 16LL * num_sms;
+}
+
+// The split count to ask for over a 4-bit cache: the least whose workspace lets
+// the batch be dealt to every SM, eight heads at a time where that can be.  One
+// CTA per row, with no merge, is left for batches of at most one row per SM whose
+// histories hold no more than a unit of 64 tokens for each of a CTA's eight warps.
+int plan_int4(int num_sms, int B, int Hkv, int longest) {
+  const long long rows = static_cast<long long>(B) * Hkv;
   if (rows <= num_sms && longest <= 8 * fd::kTile) return 1;
-  return static_cast<int>(std::clamp<long long>((2LL * num_sms + rows - 1) / rows, 2, kMaxSplits));
+  const int heads = int4_heads(num_sms, B, Hkv, kMaxSplits) ? 8 : 1;
+  return static_cast<int>(std::clamp<long long>((2LL * heads * num_sms + rows - 1) / rows, 2, kMaxSplits));
 }
 
 // The planner over every input it uses.  seqlens: host lengths or null (every
@@ -814,7 +827,7 @@ int fd_plan_problem(int num_sms, const fd_problem* p, const int32_t* seqlens) {
   if (p->kv_dtype == FD_KV_INT4) {
     int longest = p->max_len;
     if (seqlens) longest = std::min(longest, *std::max_element(seqlens, seqlens + p->B));
-    return plan_int4(num_sms, static_cast<long long>(p->B) * p->Hkv, longest);
+    return plan_int4(num_sms, p->B, p->Hkv, longest);
   }
   return plan_impl(num_sms, p->B, p->Hkv, p->D, p->max_len, p->block_size, p->kv_dtype, seqlens);
 }

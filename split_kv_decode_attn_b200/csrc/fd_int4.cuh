@@ -334,10 +334,12 @@ __device__ __forceinline__ T smem_at(const uint8_t* p) {
 }
 
 struct Int4DecodeArgs {
-  SplitArgs a;            // part_o [2 ctas, G, D] and part_lse [2 ctas, G]: see below; the
-                          // fields of the split cut, k_scale and v_scale do not apply
+  SplitArgs a;            // part_o [2 ctas heads, G, D] and part_lse [2 ctas heads, G]: see
+                          // below; the fields of the split cut, k_scale and v_scale do not apply
   int B;
   int ctas;               // CTAs the batch is dealt to (by_row: not used)
+  int groups;             // rows that the cut sees per sequence: KV heads, or eighths of them
+  int heads;              // KV heads per row of the cut: 1, or 8 (a warp each)
   bool by_row;            // one CTA per (sequence, KV head), no partial results
   bool evict_first;       // what is read leaves L2 first
 };
@@ -362,6 +364,14 @@ __device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t
 // (One CTA per split of a row, as fd_split_kernel, left a ragged batch of 32 x up
 // to 8,192 tokens at 55-58 us whatever the split count and the CTAs' shape.)
 // CTA c of C begins at c T / C of the total cost T.
+//
+// Eight heads at a time (the KV heads a multiple of 8, and a workspace for the
+// partial results): the rows of eight neighbouring KV heads, which are equally
+// long, are dealt as one, and each warp of a CTA takes its head through the CTA's
+// whole range.  The heads' rows of a token-major cache, neighbours of 64 bytes,
+// are then read at about the same time (8 x 40,000 tokens in pages of 16 at 32/8
+// heads: 42.0 us, 49.4 with the range dealt to the warps; 64 x 4,096 in pages
+// of 32 at 64/8: 50.4, 61.8), and no warp's state is merged with another's.
 //
 // Every warp works the cut out for itself from the lengths, whose first
 // kInt4Lens a CTA keeps in shared memory.  Costs stay below 2^31 (checked on the
@@ -389,8 +399,8 @@ struct Int4Cut {
   }
 };
 
-// Where a warp stands: unit u of the `units` of row (sequence b, KV head h),
-// whose sequence holds n tokens.
+// Where a warp stands: unit u of the `units` of row (sequence b, group h of KV
+// heads), whose sequence holds n tokens.
 struct Int4Walk {
   int b, h, u, units, n;
 };
@@ -398,13 +408,13 @@ struct Int4Walk {
 // The place `at` (below the total): u == units at the end of a row.  rows: the
 // rows with a token before it.
 template <int U>
-__device__ __forceinline__ Int4Walk int4_locate(const SplitArgs& a, const int* lens, int B, int lane,
+__device__ __forceinline__ Int4Walk int4_locate(const SplitArgs& a, const int* lens, int B, int groups, int lane,
                                                 uint32_t at, uint32_t& rows) {
   uint32_t before = 0, seqs = 0;
   for (int b0 = 0;; b0 += 32) {
     const int n = b0 + lane < B ? int4_length(a, lens, b0 + lane) : 0;
     const int units = (n + U - 1) / U;
-    uint32_t sum = n > 0 ? static_cast<uint32_t>(units + 1) * a.Hkv : 0u;
+    uint32_t sum = n > 0 ? static_cast<uint32_t>(units + 1) * groups : 0u;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, sum, off);
@@ -418,10 +428,10 @@ __device__ __forceinline__ Int4Walk int4_locate(const SplitArgs& a, const int* l
       w.b = b0 + l;
       w.n = __shfl_sync(0xffffffffu, n, l);
       w.units = __shfl_sync(0xffffffffu, units, l);
-      const uint32_t off = at - (before + __shfl_sync(0xffffffffu, sum, l) - (w.units + 1) * a.Hkv);
+      const uint32_t off = at - (before + __shfl_sync(0xffffffffu, sum, l) - (w.units + 1) * groups);
       w.h = static_cast<int>(off / (w.units + 1));
       w.u = static_cast<int>(off) - w.h * (w.units + 1);
-      rows = (seqs + __popc(held & ((1u << l) - 1u))) * a.Hkv + w.h;
+      rows = (seqs + __popc(held & ((1u << l) - 1u))) * groups + w.h;
       return w;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
@@ -431,10 +441,10 @@ __device__ __forceinline__ Int4Walk int4_locate(const SplitArgs& a, const int* l
 
 // To the next unit; from the last one of a row to the next row that has any.
 template <int U>
-__device__ __forceinline__ void int4_advance(const SplitArgs& a, const int* lens, int B, Int4Walk& w) {
+__device__ __forceinline__ void int4_advance(const SplitArgs& a, const int* lens, int B, int groups, Int4Walk& w) {
   if (++w.u < w.units) return;
   w.u = 0;
-  if (++w.h < a.Hkv) return;
+  if (++w.h < groups) return;
   w.h = 0;
   do {
     if (++w.b >= B) return;
@@ -555,6 +565,7 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
                ? __ldcg(a.block_table + static_cast<size_t>(at.b) * a.max_blocks_per_seq + pg)
                : 0;
   };
+  const int head = p.heads == 1 ? 0 : of;              // within the group
   int issued = 0, stage = 0;
   uint32_t phase = 1;                  // a fresh barrier counts as passed in this phase
   int page = units > 0 ? page_at() : at.b;
@@ -574,12 +585,12 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
       __syncwarp(0xffffu << (lane & 16));
       if (sub < boxes) {
         const uint32_t r = sub * box_rows;
-        tma_load_4d(st + r * L::kRowBytes, tmK, full, at.h, row, plane, policy);
-        tma_load_4d(st + L::kV + r * L::kRowBytes, tmV, full, at.h, row, plane, policy);
-        tma_load_4d(st + L::kP + r * 16, tmP, full, at.h, row, plane, policy);
+        tma_load_4d(st + r * L::kRowBytes, tmK, full, at.h * p.heads + head, row, plane, policy);
+        tma_load_4d(st + L::kV + r * L::kRowBytes, tmV, full, at.h * p.heads + head, row, plane, policy);
+        tma_load_4d(st + L::kP + r * 16, tmP, full, at.h * p.heads + head, row, plane, policy);
       }
       if (++issued < units) {
-        int4_advance<kUnit>(a, lens, p.B, at);
+        int4_advance<kUnit>(a, lens, p.B, p.groups, at);
         page = page_at();
       }
       if (++stage == kStages) {
@@ -609,9 +620,10 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
 
 // Decode attention over a 4-bit cache.  A row that lies within a warp's range is
 // finished by the warp, one within a CTA's by the CTA; of a row that goes over
-// the end of CTA c's range each CTA leaves one partial result, at index 2 c of
-// part_o and part_lse if the row began before the CTA's range (or with it),
-// otherwise at 2 c + 1, and fd_combine_int4_kernel merges them.
+// the end of CTA c's range each CTA leaves one partial result (with eight heads at
+// a time one per head), at index 2 c of part_o and part_lse if the row began
+// before the CTA's range (or with it), otherwise at 2 c + 1, and
+// fd_combine_int4_kernel merges them.
 //
 // No code is converted.  A nibble in the low four bits of a half word is the f16
 // subnormal c 2^-24 as it stands, one in the next four bits c 2^-20, both exact
@@ -659,7 +671,6 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
   volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);
   Int4Piece* pieces = reinterpret_cast<Int4Piece*>(smem + L::kRowOffset);
   const int B = p.B;
-  const bool paged = a.block_size != 0;
 
   static_assert(SH::CTAS == 1 && kInt4Warps == 8 &&
                     (kInt4Warps + kInt4CopyWarps) * kInt4StartRegs ==
@@ -716,8 +727,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     for (int b = lane; b < B; b += 32) {
       const int n = int4_length(a, lens, b);
       if (n > 0) {
-        total += static_cast<uint32_t>((n + kUnit - 1) / kUnit + 1) * a.Hkv;
-        rows += a.Hkv;
+        total += static_cast<uint32_t>((n + kUnit - 1) / kUnit + 1) * p.groups;
+        rows += p.groups;
       }
     }
 #pragma unroll
@@ -731,19 +742,20 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       cta_end = cut.begin(blockIdx.x + 1);
     }
     const uint32_t cost = cta_end - cta_begin, each = cost / kInt4Warps, rest = cost % kInt4Warps;
-    const uint32_t lo = cta_begin + each * warp + rest * warp / kInt4Warps;
-    const uint32_t hi = cta_begin + each * (warp + 1) + rest * (warp + 1) / kInt4Warps;
+    const uint32_t lo = p.heads > 1 ? cta_begin : cta_begin + each * warp + rest * warp / kInt4Warps;
+    const uint32_t hi =
+        p.heads > 1 ? cta_end : cta_begin + each * (warp + 1) + rest * (warp + 1) / kInt4Warps;
     if (lo < hi) {
       // Units before a place: its cost less the rows before it.
       uint32_t rows_lo, rows_hi = rows;
-      cur = int4_locate<kUnit>(a, lens, B, lane, lo, rows_lo);
-      if (hi < total) int4_locate<kUnit>(a, lens, B, lane, hi, rows_hi);
+      cur = int4_locate<kUnit>(a, lens, B, p.groups, lane, lo, rows_lo);
+      if (hi < total) int4_locate<kUnit>(a, lens, B, p.groups, lane, hi, rows_hi);
       mine = static_cast<int>((hi - rows_hi) - (lo - rows_lo));
       row_begin = lo - cur.u;
       if (cur.u == cur.units && mine > 0) {            // the end of a row: begin with the next
         row_begin += cur.units + 1;
         --cur.u;
-        int4_advance<kUnit>(a, lens, B, cur);
+        int4_advance<kUnit>(a, lens, B, p.groups, cur);
       }
     }
   }
@@ -753,6 +765,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
   bar_arrive(1, (kInt4Warps + kInt4CopyWarps) * 32);    // to the copying warps
   set_regs_up<kInt4ComputeRegs>();
 
+  const int head = p.heads == 1 ? 0 : warp;             // within the group
   // Word w of q of lane t4 in group h holds channels h D/2 + t4 D/8 + 8 w ..
   uint4 raw[NB][2][KW];
   auto load_q = [&]() {
@@ -760,7 +773,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     for (int nb = 0; nb < NB; ++nb) {
       const bool live = nb * 8 + g < a.G;
       const __nv_bfloat16* qrow =
-          a.q + (static_cast<size_t>(cur.b) * a.Hq + cur.h * a.G + (live ? nb * 8 + g : 0)) * D;
+          a.q + (static_cast<size_t>(cur.b) * a.Hq + (cur.h * p.heads + head) * a.G + (live ? nb * 8 + g : 0)) * D;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -1111,6 +1124,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
   const bool is_first = done == 0;
   float* f = reinterpret_cast<float*>(is_first ? smem + L::kFirstOffset + warp * L::kStateFloats * 4 : ring);
   if (!whole && !is_first) __syncwarp();               // the ring is drained, and read by every lane
+  const bool alone = p.heads > 1;                      // no other warp of the CTA has this row
+  const size_t part = (2 * static_cast<size_t>(blockIdx.x) + (row_begin > cta_begin ? 1 : 0)) * p.heads + head;
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -1122,7 +1137,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
         bias[nb][1][c] += __shfl_xor_sync(0xffffffffu, bias[nb][1][c], off);
       }
       const int col = nb * 8 + 2 * t4 + c;
-      const size_t orow = static_cast<size_t>(cur.b) * a.Hq + cur.h * a.G + col;
+      const size_t orow = static_cast<size_t>(cur.b) * a.Hq + (cur.h * p.heads + head) * a.G + col;
+      const size_t prow = part * a.G + col;
       const float inv = l_run[nb][c] == 0.f ? 0.f : 1.f / l_run[nb][c];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1135,10 +1151,16 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
           o[2 * j] = fmaf(acc[nb][h][j][c] - w8, r0, bias[nb][h][c]);
           o[2 * j + 1] = fmaf(acc[nb][h][j][c + 2] - 16.f * w8, r1, bias[nb][h][c]);
         }
-        if (!whole) {
+        if (!whole && !alone) {
 #pragma unroll
           for (int j = 0; j < 2 * MB; j += 4)
             *reinterpret_cast<float4*>(f + col * L::kAccStride + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        } else if (!whole) {
+          if (col < a.G)
+#pragma unroll
+            for (int j = 0; j < 2 * MB; j += 4)
+              *reinterpret_cast<float4*>(a.part_o + prow * D + d + j) =
+                  make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
         } else if (col < a.G) {
           uint32_t w[MB];
 #pragma unroll
@@ -1150,15 +1172,18 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
         }
       }
       if (g == 0) {
-        if (!whole) {
+        const float lse = (ref[nb][c] + log2f(l_run[nb][c])) * 0.69314718055994530942f;
+        if (!whole && !alone) {
           f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
           f[L::kL + col] = l_run[nb][c];
+        } else if (!whole) {
+          if (col < a.G) a.part_lse[prow] = lse;
         } else if (col < a.G && a.lse) {
-          a.lse[orow] = (ref[nb][c] + log2f(l_run[nb][c])) * 0.69314718055994530942f;
+          a.lse[orow] = lse;
         }
       }
     }
-  if (!whole && lane == 0) {
+  if (!whole && !alone && lane == 0) {
     Int4Piece& pc = pieces[2 * warp + (is_first ? 0 : 1)];
     pc.row = static_cast<long long>(cur.b) * a.Hkv + cur.h;
     pc.begin = row_begin;
@@ -1168,7 +1193,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
   if (done < mine) {
     row_begin += cur.units + 1;
     cur.u += count - 1;
-    int4_advance<kUnit>(a, lens, B, cur);
+    int4_advance<kUnit>(a, lens, B, p.groups, cur);
     load_q();
   }
   }
@@ -1251,57 +1276,79 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
 
 constexpr int kInt4CombineWarps = 4;
 
-// Merges the partial results of rows that several CTAs share: one warp per (CTA,
-// query head of a group), which takes the row that begins in the CTA's range and
-// goes on beyond, its lanes over D.
-template <int D, int U>
+// Merges the partial results of rows that several CTAs share: SHARE warps (one or
+// the CTA's four) per query head of a row, their lanes over D.  The candidates are
+// the rows themselves or, when there are fewer CTAs than rows, the row that begins
+// in each CTA's range and goes on beyond.  A warp requests BATCH partial results at
+// once.
+template <int D, int U, int SHARE, int BATCH>
 __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel(const Int4DecodeArgs p) {
-  constexpr int VPL = D / 32, BATCH = 32;
+  constexpr int VPL = D / 32;
   constexpr float kLog2e = 1.4426950408889634074f;
   __shared__ int lens[kInt4Lens];
   const SplitArgs& a = p.a;
   const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * kInt4CombineWarps + (threadIdx.x >> 5);
-  const uint32_t cta = w / a.G;
+  const int w = blockIdx.x * (kInt4CombineWarps / SHARE) + (threadIdx.x >> 5) / SHARE;
+  const int share = (threadIdx.x >> 5) % SHARE;        // this warp takes parts share + i SHARE
+  const int per = p.heads * a.G;       // query heads of a candidate
+  const int cand = w / per, head = w - cand * per;
   // The lengths may be read before the wait, as fd_combine_kernel reads them.
   for (int b = threadIdx.x; b < min(p.B, kInt4Lens); b += kInt4CombineWarps * 32) lens[b] = int4_length(a, b);
   __syncthreads();
-  uint32_t total = 0;
+  const bool by_rows = p.B * p.groups <= p.ctas;
+  const int cand_b = by_rows ? cand / p.groups : 0;
+  uint32_t total = 0, before = 0;      // costs of all rows, of the sequences before cand_b
   for (int b = lane; b < p.B; b += 32) {
     const int n = int4_length(a, lens, b);
-    if (n > 0) total += static_cast<uint32_t>((n + U - 1) / U + 1) * a.Hkv;
+    const uint32_t cost = n > 0 ? static_cast<uint32_t>((n + U - 1) / U + 1) * p.groups : 0u;
+    total += cost;
+    if (b < cand_b) before += cost;
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  for (int off = 16; off > 0; off >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, off);
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+  }
   const Int4Cut cut{total, min(static_cast<uint32_t>(p.ctas), total)};
-  int parts = 0;
-  bool begins = false;                 // with the CTA's range
-  Int4Walk row{};
-  if (cta + 1 < cut.ctas) {
+  int parts = 0, row_b = cand_b, row_h = cand - cand_b * p.groups;
+  uint32_t first = 0;                  // the CTA with the row's first part
+  bool begins = false;                 // with that CTA's range
+  if (by_rows) {
+    const int n = cand_b < p.B ? int4_length(a, lens, cand_b) : 0;
+    if (n > 0) {
+      const uint32_t units = (n + U - 1) / U, begin = before + row_h * (units + 1);
+      first = cut.holder(begin);
+      parts = static_cast<int>(cut.holder(begin + units - 1) - first) + 1;
+      begins = begin == cut.begin(first);
+      if (begin + units <= cut.begin(first + 1)) parts = 0;   // one CTA's, finished there
+    }
+  } else if (cand + 1 < static_cast<int>(cut.ctas)) {
     uint32_t rows;
-    const uint32_t at = cut.begin(cta + 1), from = cut.begin(cta);
-    row = int4_locate<U>(a, lens, p.B, lane, at, rows);
+    first = cand;
+    const uint32_t at = cut.begin(first + 1), from = cut.begin(first);
+    const Int4Walk row = int4_locate<U>(a, lens, p.B, p.groups, lane, at, rows);
     const uint32_t begin = at - row.u;
     if (row.u > 0 && row.u < row.units && begin >= from) {
-      parts = static_cast<int>(cut.holder(begin + row.units - 1) - cta) + 1;
+      parts = static_cast<int>(cut.holder(begin + row.units - 1) - first) + 1;
       begins = begin == from;
+      row_b = row.b;
+      row_h = row.h;
     }
   }
   grid_dependency_wait();     // partial results come from the kernel before
   grid_dependents_launch();
   if (parts == 0) return;
-  const int head = w - static_cast<int>(cta) * a.G;
-  const size_t r = (static_cast<size_t>(row.b) * a.Hkv + row.h) * a.G + head;
+  const size_t r = static_cast<size_t>(row_b) * a.Hq + row_h * per + head;
   auto index = [&](int i) {            // of part i
-    return static_cast<size_t>(i == 0 && !begins ? 2 * cta + 1 : 2 * (cta + i)) * a.G + head;
+    return static_cast<size_t>(i == 0 && !begins ? 2 * first + 1 : 2 * (first + i)) * per + head;
   };
-  // The first 32 parts are requested at once, with their log-sum-exps.
+  // The first parts are requested at once, with their log-sum-exps.
   float lb[BATCH], ob[BATCH][VPL];
   auto load = [&](int s) {
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
-      if (s + j < parts) {
-        const size_t x = index(s + j);
+      if (s + j * SHARE < parts) {
+        const size_t x = index(s + j * SHARE);
         lb[j] = __ldcg(a.part_lse + x);
         if constexpr (VPL == 4) {
           const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + x * D) + lane);
@@ -1312,7 +1359,7 @@ __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel
         }
       }
   };
-  load(0);
+  load(share);
   float mx = -INFINITY;
   bool nan = false;
   for (int i = lane; i < parts; i += 32) {
@@ -1326,16 +1373,29 @@ __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel
   float W = 0.f, acc[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
-  for (int s = 0; s < parts; s += BATCH) {
-    if (s > 0) load(s);
+  for (int s = share; s < parts; s += BATCH * SHARE) {
+    if (s > share) load(s);
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
-      if (s + j < parts) {
+      if (s + j * SHARE < parts) {
         const float wt = mx == -INFINITY ? 0.f : ex2((lb[j] - mx) * kLog2e);
         W += wt;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) acc[i] += wt * ob[j][i];
       }
+  }
+  if constexpr (SHARE > 1) {
+    __shared__ float sums[SHARE][D + 1];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sums[share][lane * VPL + i] = acc[i];
+    if (lane == 0) sums[share][D] = W;
+    __syncthreads();
+    if (share > 0) return;
+    for (int s = 1; s < SHARE; ++s) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] += sums[s][lane * VPL + i];
+      W += sums[s][D];
+    }
   }
   const float inv = W == 0.f ? 0.f : 1.f / W;
   if constexpr (VPL == 4)

@@ -131,6 +131,19 @@ fd_status launch_split_int4(const Int4Maps& m, const fd::Int4DecodeArgs& a, dim3
   return launch_chained(kern, grid, (SH::WARPS + fd::kInt4CopyWarps) * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
 }
 
+// Rows of many parts (on average) are merged by four warps per query head, which
+// ask for 64 of them at once; otherwise by one, with more of them resident.
+template <int D, int U>
+fd_status launch_combine_int4(const fd::Int4DecodeArgs& d, int rows, fd_stream_t s) {
+  const int cand = std::min(rows, d.ctas);
+  const bool many = d.ctas > 10 * cand;
+  const long long warps = static_cast<long long>(cand) * d.heads * d.a.G * (many ? fd::kInt4CombineWarps : 1);
+  const dim3 grid(static_cast<unsigned>((warps + fd::kInt4CombineWarps - 1) / fd::kInt4CombineWarps));
+  const int threads = fd::kInt4CombineWarps * 32;
+  return many ? launch_chained(fd::fd_combine_int4_kernel<D, U, fd::kInt4CombineWarps, 16>, grid, threads, 0, s, d)
+              : launch_chained(fd::fd_combine_int4_kernel<D, U, 1, 8>, grid, threads, 0, s, d);
+}
+
 // Do two arrays of int32 share memory?
 bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
@@ -273,18 +286,18 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.scale_log2 = scale * 1.4426950408889634074f;
   a.scale = scale;
   d.B = p->B;
-  // Two partial results per CTA have to fit the workspace; more than one CTA per
-  // SM would wait for a place.
   int sms = 0;
   if (device_sms(dev, &sms) != FD_OK) return FD_ERR_CUDA;
   const long long rows = static_cast<long long>(p->B) * p->Hkv;
   if (rows * ((p->max_len + unit - 1LL) / unit + 1) > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
   d.by_row = num_splits == 1;
   d.evict_first = !c.nhd;
+  d.heads = !d.by_row && int4_heads(sms, p->B, p->Hkv, num_splits) ? 8 : 1;
+  d.groups = p->Hkv / d.heads;
   if (!d.by_row) {
-    d.ctas = int4_ctas(sms, rows, num_splits);
+    d.ctas = d.heads > 1 ? sms : int4_ctas(sms, rows, num_splits);
     a.part_o = static_cast<float*>(workspace);
-    a.part_lse = a.part_o + static_cast<size_t>(2) * d.ctas * a.G * p->D;
+    a.part_lse = a.part_o + static_cast<size_t>(2) * d.ctas * d.heads * a.G * p->D;
   }
   const dim3 grid = d.by_row ? dim3(static_cast<unsigned>(p->Hkv), static_cast<unsigned>(p->B))
                              : dim3(static_cast<unsigned>(d.ctas));
@@ -296,14 +309,13 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
     r = a.G <= 8 ? launch_split_int4<64, 1, ShapeN>(maps, d, grid, dev, stream)
                  : launch_split_int4<64, 2, ShapeW>(maps, d, grid, dev, stream);
   if (r == FD_OK && !d.by_row && d.ctas > 1) {
-    const dim3 cgrid(static_cast<unsigned>((d.ctas * a.G + fd::kInt4CombineWarps - 1) / fd::kInt4CombineWarps));
-    const int threads = fd::kInt4CombineWarps * 32;
+    const int cut_rows = static_cast<int>(rows / d.heads);
     if (p->D == 128)
-      r = unit == 64 ? launch_chained(fd::fd_combine_int4_kernel<128, 64>, cgrid, threads, 0, stream, d)
-                     : launch_chained(fd::fd_combine_int4_kernel<128, 32>, cgrid, threads, 0, stream, d);
+      r = unit == 64 ? launch_combine_int4<128, 64>(d, cut_rows, stream)
+                     : launch_combine_int4<128, 32>(d, cut_rows, stream);
     else
-      r = unit == 64 ? launch_chained(fd::fd_combine_int4_kernel<64, 64>, cgrid, threads, 0, stream, d)
-                     : launch_chained(fd::fd_combine_int4_kernel<64, 32>, cgrid, threads, 0, stream, d);
+      r = unit == 64 ? launch_combine_int4<64, 64>(d, cut_rows, stream)
+                     : launch_combine_int4<64, 32>(d, cut_rows, stream);
   }
   return r;
 }

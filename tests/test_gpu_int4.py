@@ -209,6 +209,29 @@ def test_contiguous_token_major_and_odd_lengths(Hkv):
             check(*decode(c, S), ref, f"Hkv={Hkv} layout={layout} S={S}")
 
 
+@pytest.mark.parametrize("layout", [HND, NHD])
+@pytest.mark.parametrize("G,D,Hkv,bs", [(1, 64, 8, 0), (4, 128, 8, 16), (8, 128, 16, 32),
+                                        (16, 128, 8, 8), (16, 64, 8, 0)])
+def test_eight_heads_at_a_time(G, D, Hkv, bs, layout):
+    """KV heads in eights: one row of up to 150 parts, several in one range."""
+    lens = [0, 1, 5000, 64, 65, 300, 1000, 0]
+    c = Cache(lens, G * Hkv, Hkv, D, 5000 if bs == 0 else 5024, seed=900 + G + D, block_size=bs,
+              layout=layout).on_device()
+    ref = c.oracle()
+    for S in (None, 2, 40, 1024):
+        check(*decode(c, S), ref, f"G={G} D={D} Hkv={Hkv} bs={bs} layout={layout} S={S}")
+
+
+@pytest.mark.parametrize("B,most", [(200, 100), (700, 40)])
+def test_eight_heads_of_many_sequences(B, most):
+    r = np.random.default_rng(B)
+    lens = r.integers(0, most + 1, B).tolist()
+    c = Cache(lens, 8, 8, 64, most, seed=B).on_device()
+    ref = c.oracle()
+    for S in (None, 1, 16):
+        check(*decode(c, S), ref, f"B={B} S={S}")
+
+
 def test_seqlens_are_clamped_and_optional():
     c = Cache([90, 90], 8, 1, 64, 90, seed=9).on_device()
     ref = c.oracle()

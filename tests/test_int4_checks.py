@@ -129,16 +129,17 @@ def test_page_refusals():
 
 def test_planner_takes_4_bit_caches():
     """The least count whose workspace serves a CTA on each of the 148 SMs (two
-    partial results each, B Hkv S / 2 CTAs); short histories of few rows keep one
-    CTA per row."""
+    partial results each; two for each of eight KV heads with Hkv a multiple of 8
+    and five such rows); short histories of few rows keep one CTA per row."""
     def plan(B, Hkv, L, lens=None, D=128):
         return fd.fd_plan_problem(148, fd.make_problem(B, 8 * Hkv, Hkv, D, L, kv_dtype=fd.FD_KV_INT4),
                                   lens)
-    for B, Hkv in ((1, 1), (1, 8), (3, 5), (32, 8), (64, 8), (4096, 8)):
+    for B, Hkv, heads in ((1, 1, 1), (1, 8, 1), (4, 8, 1), (3, 5, 1), (9, 12, 1), (5, 8, 8),
+                          (2, 16, 1), (3, 16, 8), (32, 8, 8), (64, 8, 8), (4096, 8, 8)):
         S = plan(B, Hkv, 65536)
         assert 2 <= S <= 1024
-        assert B * Hkv * S // 2 >= 148
-        assert S == 2 or B * Hkv * (S - 1) // 2 < 148
+        assert B * Hkv * S // (2 * heads) >= 148
+        assert S == 2 or B * Hkv * (S - 1) // (2 * heads) < 148
     assert plan(1, 8, 0) == plan(1, 8, 1) == plan(1, 8, 512) == plan(18, 8, 512, D=64) == 1
     assert plan(1, 8, 513) > 1 and plan(19, 8, 512) > 1
     assert plan(2, 8, 65536, [512, 7]) == 1 and plan(2, 8, 65536, [513, 7]) > 1

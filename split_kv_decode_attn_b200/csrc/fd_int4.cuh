@@ -603,6 +603,7 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
       if (since == 0) since = now;
       failed = now - since > kWaitLimitNs;
     }
+    if (!__any_sync(0xffffffffu, ready)) __nanosleep(100);   // leave the issue slots to the others
     __syncwarp();
   }
   volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);

@@ -141,8 +141,10 @@ def test_planner_takes_4_bit_caches():
         assert B * Hkv * S // (2 * heads) >= 148
         assert S == 2 or B * Hkv * (S - 1) // (2 * heads) < 148
     assert plan(1, 8, 0) == plan(1, 8, 1) == plan(1, 8, 512) == plan(18, 8, 512, D=64) == 1
-    assert plan(1, 8, 513) > 1 and plan(19, 8, 512) > 1
-    assert plan(2, 8, 65536, [512, 7]) == 1 and plan(2, 8, 65536, [513, 7]) > 1
+    assert plan(1, 8, 1536) == 1 and plan(1, 8, 1537) > 1 and plan(19, 8, 512) > 1
+    assert plan(2, 8, 65536, [1536, 7]) == 1 and plan(2, 8, 65536, [1537, 7]) > 1
+    assert plan(18, 8, 4096) == 1 and plan(18, 8, 65536) > 1
+    assert plan(18, 8, 4096, [4096] + 17 * [7]) > 1
     assert plan(2, 8, 65536, [-4, 0]) == 1
     assert fd.fd_plan_problem(148, P(D=96)) == UNSUP
 

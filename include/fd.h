@@ -169,9 +169,10 @@ FD_API int fd_plan_seqlens(int num_sms, int B, int Hq, int Hkv, int D, int max_l
 
 /* The planner for a whole problem description: the same cost model, with
  * the cache's element type (an fp8 CTA moves half the bytes of a bf16 one
- * at the same token rate, so fp8 caches want more CTAs in flight; a 4-bit one
- * about a quarter) and, when given, the lengths. fd_plan and fd_plan_seqlens
- * plan for bf16 caches.
+ * at the same token rate, so fp8 caches want more CTAs in flight) and, when
+ * given, the lengths. For a 4-bit cache it gives 1 where one CTA per row serves
+ * best, and otherwise the least count whose workspace lets fd_decode_int4 use
+ * every SM. fd_plan and fd_plan_seqlens plan for bf16 caches.
  *   num_sms   SM count to plan for; <= 0 means the current device's
  *   p         HOST pointer to the problem as passed to fd_decode (pointers
  *             and scales are not read)
@@ -402,9 +403,9 @@ FD_API fd_status fd_append_int4(const fd_problem* p, int n_tokens, const void* k
                                 fd_stream_t stream);
 
 /* The rows of a 4-bit cache as a contiguous bf16 cache: s (c - 8) + b, rounded
- * once. The result is a cache for fd_decode and the entry
- * points beside it, and what the attention of a prompt reads when it is to see
- * the same K and V as the later steps.
+ * once. The result is a cache for fd_decode and the entry points beside it, and
+ * what the attention of a prompt reads when it is to see the same K and V as the
+ * later steps.
  *   k4, v4, params, seqlens, block_table   as for fd_decode_int4
  *   k_out, v_out   bf16, 16-byte aligned: [B, Hkv, max_len, D]
  *                  (FD_LAYOUT_HND) or [B, max_len, Hkv, D] (FD_LAYOUT_NHD),
@@ -417,12 +418,26 @@ FD_API fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void*
                                 fd_stream_t stream);
 
 /* Decode attention over a 4-bit cache: fd_decode over the values that the
- * codes stand for. D is 64 or 128; G, layouts, pages, lengths, the split cut,
- * the workspace and the results are those of fd_decode (fd_plan_problem gives
- * the split count). Scores and sums are taken in fp32; a softmax weight enters
- * the product with V's codes as weight * scale, rounded to f16 (11 significant
- * bits) relative to the largest scale seen. Rows at or past a sequence's
- * length may hold anything. A page id outside [0, num_blocks) reads zeros. */
+ * codes stand for. D is 64 or 128; G, layouts, pages, lengths, scale, out and lse
+ * are as for fd_decode, and rows at or past a sequence's length may hold
+ * anything. A page id outside [0, num_blocks) reads zeros. max_len is at most
+ * 0x7fffff00, and B * Hkv * (max_len / 32 + 2) below 2^31
+ * (FD_ERR_INVALID_ARGUMENT otherwise).
+ *   num_splits  1: one CTA per (sequence, KV head), no workspace. Above 1 the
+ *               tokens of the whole batch are dealt evenly to the SMs, whatever
+ *               the lengths, and a second kernel merges what a row's CTAs have;
+ *               the count only says how large a workspace there is: with fewer
+ *               than fd_plan_problem's, fewer CTAs may share the work. At most
+ *               1024.
+ *   workspace   fd_workspace_bytes(B, Hq, D, num_splits) bytes for num_splits
+ *               above 1 (FD_ERR_WORKSPACE if it is smaller); nothing is kept in it
+ *               between calls.
+ * Scores and sums are taken in fp32. A softmax weight enters the product with V's
+ * codes as weight * scale in f16 (11 significant bits), relative to a power of
+ * two above the largest V scale that its warp has seen. The result of a call is
+ * the same bits every time; how a sequence's sum is split over CTAs, and with it
+ * the last bits of its result, depends on the other sequences' lengths when
+ * num_splits is above 1, but not on the order of the cache's dimensions or pages. */
 FD_API fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4,
                                 const void* v4, const void* params, const int32_t* seqlens,
                                 const int32_t* block_table, float scale, int num_splits,

@@ -9,7 +9,7 @@
 // waiting between CTAs, and no atomics, so the result is a function of the
 // inputs alone.  What bounds them is latency: 3.0-3.1 us a launch from graph
 // replays for 16 requests, 4.1 for 1,024 (two sums of 10 exchanges each and three
-// barriers per pass) and 5.9 for 500,000 tokens of 200 prompts (6 MB written).
+// barriers per pass) and 5.9 for 250,000 tokens of 200 prompts (3 MB written).
 // Inputs are read through L2, where the kernel before left them.
 #pragma once
 

@@ -216,6 +216,7 @@ B, Hkv, G, D, bs, blocks = 6, 8, 2, 128, 16, 20
 i32 = dict(dtype=torch.int32, device="cuda")
 k4 = torch.zeros(B * blocks, Hkv, bs, D // 2, dtype=torch.uint8, device="cuda")
 v4, prm = torch.zeros_like(k4), torch.zeros(B * blocks, Hkv, bs, 8, dtype=torch.bfloat16, device="cuda")
+torch.manual_seed(0)
 x = torch.randn(100 * B, Hkv, D, device="cuda").to(torch.bfloat16)
 q = torch.randn(B, Hkv * G, D, device="cuda").to(torch.bfloat16)
 lens, new, done = torch.zeros(B, **i32), torch.full((B,), 100, **i32), torch.zeros(B, dtype=torch.uint8, device="cuda")
@@ -242,8 +243,12 @@ for turn in range(3):
     n = 100 * (turn + 1)
     assert lens.tolist() == [n] * B and int(count) == B * (blocks - -(-n // bs))
     assert (ko[:, :, :n].float() - x.view(B, 100, Hkv, D).transpose(1, 2).repeat(1, 1, turn + 1, 1).float()).abs().max() < 0.5
-    for out in outs.values():   # two roundings to bf16 below 1, 2^-9 each, and the weights' 2^-11 of |v|, mean 0.8
-        assert outs[1].abs().max() < 1 and (out.float() - outs[1].float()).abs().max() < 6e-3, turn
+    # Two roundings to bf16, 2^-9 each below 1 and 2^-8 from 1 to 2, and the weights' 2^-11 of |v|, mean 0.8, twice
+    # (below 1: 2 2^-9 + 2 2^-11 0.8 = 4.7e-3; from 1 to 2: 2 2^-8 + 2 2^-11 0.8 = 8.6e-3).
+    top = outs[1].float().abs().max().item()
+    assert top < 2
+    for out in outs.values():
+        assert (out.float() - outs[1].float()).abs().max() < (6e-3 if top < 1 else 9e-3), turn
 assert fd.fd_check_device_error() == fd.FD_OK
 print("fine")
 """

@@ -574,7 +574,9 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
   while (__any_sync(0xffffffffu, issued < units && !failed)) {
     const bool more = issued < units && !failed;
     const uint32_t full = bar + 8 * stage;
-    const bool ready = more && mbar_test(full + L::kFreeBars, phase);
+    // The lanes of a ring go on together: each has seen its stage free, or none goes.
+    const unsigned seen = __ballot_sync(0xffffffffu, more && mbar_test(full + L::kFreeBars, phase));
+    const bool ready = ((seen >> (lane & kHalf)) & 0xffffu) == 0xffffu;
     if (ready) {
       const int t0 = at.u * kUnit;
       const uint32_t st = ring + stage * L::kStageBytes;
@@ -603,7 +605,7 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
       if (since == 0) since = now;
       failed = now - since > kWaitLimitNs;
     }
-    if (!__any_sync(0xffffffffu, ready)) __nanosleep(100);   // leave the issue slots to the others
+    if (seen == 0) __nanosleep(100);                   // leave the issue slots to the others
     __syncwarp();
   }
   volatile int* cta_error = reinterpret_cast<volatile int*>(smem + L::kErrorOffset);

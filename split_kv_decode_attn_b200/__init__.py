@@ -18,6 +18,7 @@ from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfd.so")
+CALLS_PATH = os.path.join(_HERE, "_fdcall.so")
 
 FD_OK = 0
 FD_ERR_INVALID_ARGUMENT = -1
@@ -129,8 +130,23 @@ def load_library(path: str = LIB_PATH):
     return _lib
 
 
-def _lib_():
-    return _lib if _lib is not None else load_library()
+_calls = None
+
+
+def _load_calls():
+    """The calls whose time on the host counts (csrc/fdcall.c), on the library's
+    functions."""
+    global _calls
+    if _calls is None:
+        lib = load_library()
+        if not os.path.exists(CALLS_PATH):
+            raise ImportError(f"{CALLS_PATH} is missing; build it with __graft_entry__.build()")
+        from . import _fdcall
+        _fdcall.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                       (lib.fd_append_int4, lib.fd_expand_int4, lib.fd_decode_int4,
+                        lib.fd_alloc_pages, lib.fd_release_pages)))
+        _calls = _fdcall
+    return _calls
 
 
 def _ptr(x) -> Optional[int]:
@@ -243,18 +259,17 @@ def fd_append_int4(problem: fd_problem, n_tokens: int, k_new, k_stride: int, v_n
     """Call the C fd_append_int4: quantise new rows and write them at their
     slots.  Strides count elements from one token to the next.  Returns the
     status."""
-    return _lib_().fd_append_int4(ctypes.byref(problem), n_tokens, _ptr(k_new), k_stride,
-                                  _ptr(v_new), v_stride, _ptr(slots), _ptr(k4), _ptr(v4),
-                                  _ptr(params), _stream(stream))
+    return (_calls or _load_calls()).append_int4(problem, n_tokens, k_new, k_stride, v_new,
+                                                 v_stride, slots, k4, v4, params,
+                                                 _stream(stream))
 
 
 def fd_expand_int4(problem: fd_problem, k4, v4, params, seqlens, block_table, k_out, v_out,
                    stream=None) -> int:
     """Call the C fd_expand_int4: a 4-bit cache as a contiguous bf16 cache.
     Returns the status."""
-    return _lib_().fd_expand_int4(ctypes.byref(problem), _ptr(k4), _ptr(v4), _ptr(params),
-                                  _ptr(seqlens), _ptr(block_table), _ptr(k_out), _ptr(v_out),
-                                  _stream(stream))
+    return (_calls or _load_calls()).expand_int4(problem, k4, v4, params, seqlens, block_table,
+                                                 k_out, v_out, _stream(stream))
 
 
 def fd_decode_int4(problem: fd_problem, q, k4, v4, params, seqlens, block_table, scale: float,
@@ -262,10 +277,9 @@ def fd_decode_int4(problem: fd_problem, q, k4, v4, params, seqlens, block_table,
                    stream=None) -> int:
     """Call the C fd_decode_int4: decode attention over a 4-bit cache.  Returns
     the status."""
-    return _lib_().fd_decode_int4(ctypes.byref(problem), _ptr(q), _ptr(k4), _ptr(v4),
-                                  _ptr(params), _ptr(seqlens), _ptr(block_table), scale,
-                                  num_splits, _ptr(out), _ptr(lse), _ptr(workspace),
-                                  workspace_bytes, _stream(stream))
+    return (_calls or _load_calls()).decode_int4(problem, q, k4, v4, params, seqlens,
+                                                 block_table, scale, num_splits, out, lse,
+                                                 workspace, workspace_bytes, _stream(stream))
 
 
 def fd_alloc_pages(B: int, block_size: int, max_blocks_per_seq: int, max_tokens: int,
@@ -273,11 +287,11 @@ def fd_alloc_pages(B: int, block_size: int, max_blocks_per_seq: int, max_tokens:
                    seqlens_out, cu_new, slots, positions, free_count_out, stream=None) -> int:
     """Call the C fd_alloc_pages: pages, slots and positions for the new tokens
     of a batch.  Returns the status."""
-    return _lib_().fd_alloc_pages(B, block_size, max_blocks_per_seq, max_tokens, num_pages,
-                                  _ptr(seqlens), _ptr(new_lens), _ptr(free_pages),
-                                  _ptr(free_count), _ptr(block_table), _ptr(seqlens_out),
-                                  _ptr(cu_new), _ptr(slots), _ptr(positions),
-                                  _ptr(free_count_out), _stream(stream))
+    return (_calls or _load_calls()).alloc_pages(B, block_size, max_blocks_per_seq, max_tokens,
+                                                 num_pages, seqlens, new_lens, free_pages,
+                                                 free_count, block_table, seqlens_out, cu_new,
+                                                 slots, positions, free_count_out,
+                                                 _stream(stream))
 
 
 def fd_release_pages(B: int, block_size: int, max_blocks_per_seq: int, num_pages: int, seqlens,
@@ -285,10 +299,10 @@ def fd_release_pages(B: int, block_size: int, max_blocks_per_seq: int, num_pages
                      stream=None) -> int:
     """Call the C fd_release_pages: pages of finished requests back to the
     pool.  Returns the status."""
-    return _lib_().fd_release_pages(B, block_size, max_blocks_per_seq, num_pages, _ptr(seqlens),
-                                    _ptr(done), _ptr(block_table), _ptr(free_pages),
-                                    _ptr(free_count), _ptr(seqlens_out), _ptr(free_count_out),
-                                    _stream(stream))
+    return (_calls or _load_calls()).release_pages(B, block_size, max_blocks_per_seq, num_pages,
+                                                   seqlens, done, block_table, free_pages,
+                                                   free_count, seqlens_out, free_count_out,
+                                                   _stream(stream))
 
 
 def fd_combine(R: int, B: int, Hq: int, D: int, part_o, part_lse, out, lse, stream=None) -> int:

@@ -1,15 +1,18 @@
-"""Build libfd.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc."""
+"""Build libfd.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and
+_fdcall.so (Python's calls of a part of it, csrc/fdcall.c) with gcc."""
 from __future__ import annotations
 
 import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfd.so")
+CALLS = os.path.join(HERE, "_fdcall.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -37,9 +40,20 @@ def deps():
         os.path.join(ROOT, "include", "fd.h")]
 
 
+def build_calls(force: bool = False) -> str:
+    src, header = os.path.join(CSRC, "fdcall.c"), os.path.join(ROOT, "include", "fd.h")
+    if (force or not os.path.exists(CALLS)
+            or os.path.getmtime(CALLS) < max(os.path.getmtime(src), os.path.getmtime(header))):
+        subprocess.check_call(["gcc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC",
+                               "-I", os.path.join(ROOT, "include"),
+                               "-I", sysconfig.get_paths()["include"], src, "-o", CALLS])
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/*.cu into split_kv_decode_attn_b200/libfd.so (skipped when
-    the library is newer than every source)."""
+    the library is newer than every source), and csrc/fdcall.c beside it."""
+    build_calls(force)
     if not force and os.path.exists(LIB):
         newest = max(os.path.getmtime(p) for p in deps())
         if os.path.getmtime(LIB) >= newest:

@@ -170,7 +170,7 @@ FD_API int fd_plan_seqlens(int num_sms, int B, int Hq, int Hkv, int D, int max_l
 /* The planner for a whole problem description: the same cost model, with
  * the cache's element type (an fp8 CTA moves half the bytes of a bf16 one
  * at the same token rate, so fp8 caches want more CTAs in flight) and, when
- * given, the lengths. For a 4-bit cache it gives 1 where one CTA per row serves
+ * given, the lengths. For a 4-bit cache it gives 1 where one cluster per row serves
  * best, and otherwise the least count whose workspace lets fd_decode_int4 use
  * every SM. fd_plan and fd_plan_seqlens plan for bf16 caches.
  *   num_sms   SM count to plan for; <= 0 means the current device's
@@ -423,7 +423,8 @@ FD_API fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void*
  * anything. A page id outside [0, num_blocks) reads zeros. max_len is at most
  * 0x7fffff00, and B * Hkv * (max_len / 32 + 2) below 2^31
  * (FD_ERR_INVALID_ARGUMENT otherwise).
- *   num_splits  1: one CTA per (sequence, KV head), no workspace. Above 1 the
+ *   num_splits  1: one thread-block cluster per (sequence, KV head), of one to
+ *               eight CTAs by the sizes in p, and no workspace. Above 1 the
  *               tokens of the whole batch are dealt evenly to the SMs, whatever
  *               the lengths, and a second kernel merges what a row's CTAs have;
  *               the count only says how large a workspace there is: with fewer

@@ -649,7 +649,7 @@ def decode_int4(q, k4, v4, params, seqlens=None, block_table=None, *,
     orders of decode()'s caches (include/fd.h has the format; append_int4 fills
     it).  Paged caches come with block_table [B, max_blocks] int32.  seqlens
     [B] int32 or None.  Returns (out [B, Hq, D] bf16, lse [B, Hq] fp32).
-    num_splits (1: one CTA per row; above, the batch is dealt to the SMs) defaults
+    num_splits (1: one cluster per row; above, the batch is dealt to the SMs) defaults
     to fd_plan_problem's choice.  Raises ValueError for tensors of the wrong dtype,
     shape or device, or not contiguous, before anything is launched, and FdError for
     a failing status."""

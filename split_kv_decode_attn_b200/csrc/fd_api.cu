@@ -737,16 +737,32 @@ bool int4_heads(int num_sms, int B, int Hkv, int num_splits) {
          static_cast<long long>(B) * Hkv * num_splits >= 16LL * num_sms;
 }
 
+// CTAs that share a row when no workspace is used (num_splits = 1), as one cluster:
+// as many as stay resident for all rows, and no more than take a round less. kFit:
+// clusters of C = 1 .. 8 CTAs, one CTA per SM, that 148 SMs hold at once
+// (cudaOccupancyMaxActiveClusters; a cluster lies within one group of SMs).
+int int4_cluster(int num_sms, long long rows, int longest) {
+  static constexpr int kFit[fd::kInt4MaxCluster] = {148, 74, 45, 33, 26, 22, 15, 15};
+  const long long round = 8 * fd::kTile;             // tokens of one round of a CTA
+  int c = fd::kInt4MaxCluster;
+  while (c > 1 && rows * 148 > static_cast<long long>(kFit[c - 1]) * num_sms) --c;
+  const long long rounds = std::max(1LL, (longest + c * round - 1) / (c * round));
+  return static_cast<int>(std::clamp((longest + rounds * round - 1) / (rounds * round), 1LL, static_cast<long long>(c)));
+}
+
 // The split count to ask for over a 4-bit cache: the least whose workspace lets
 // the batch be dealt to every SM, eight heads at a time where that can be.  One
-// CTA per row, with no merge, takes a round of 8 x 64 tokens at a time, the longest
-// row the most; dealing takes the mean over the SMs and, for the cut and the merge,
-// about three rounds more (1 x 1,536 tokens at 64/8 heads: 10.7 us against 10.9,
-// 1 x 2,048 12.7 against 11.2, 16 x 2,048 14.8 against 18.8; a launch is saved too).
+// cluster per row, with no second kernel, takes a round of C x 8 x 64 tokens at a time,
+// the longest row the most; dealing takes the mean over the SMs and, for the cut and
+// the merge, about three rounds more, two more than a cluster's merge (64/8 heads, graph
+// replays, clusters against dealt: 1 x 2,048 7.9 and 11.1 us, 1 x 12,288 12.5 and 13.7,
+// 1 x 16,384 14.5 and 14.3, 2 x 8,192 12.7 and 15.6; one CTA per row: 16 x 2,048 14.1
+// and 18.1, 16 x up to 4,096 21.6 and 19.3; a launch of the host is saved too).
 int plan_int4(int num_sms, int B, int Hkv, int longest, long long tokens) {
   const long long rows = static_cast<long long>(B) * Hkv, round = 8 * fd::kTile;
-  const long long rounds = (std::max(longest, 0) + round - 1) / round;
-  if (rows <= num_sms && (rounds - 3) * round * num_sms <= tokens * Hkv) return 1;
+  const int c = int4_cluster(num_sms, rows, std::max(longest, 0));
+  const long long rounds = (std::max(longest, 0) + c * round - 1) / (c * round) - (c > 1 ? 2 : 3);
+  if (rows <= num_sms && rounds * round * num_sms <= tokens * Hkv) return 1;
   const int heads = int4_heads(num_sms, B, Hkv, kMaxSplits) ? 8 : 1;
   return static_cast<int>(std::clamp<long long>((2LL * heads * num_sms + rows - 1) / rows, 2, kMaxSplits));
 }

@@ -328,10 +328,38 @@ __device__ __forceinline__ void set_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Between the CTAs of a cluster: what was written to shared memory before the arrival
+// is there for all after the wait (threads that have ended count as arrived).
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of this CTA's `at` in CTA `rank` of the cluster, and loads from there.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t at, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
 template <class T>
 __device__ __forceinline__ T smem_at(const uint8_t* p) {
   return *reinterpret_cast<const T*>(p);
 }
+
+constexpr int kInt4MaxCluster = 8;    // the portable limit
 
 struct Int4DecodeArgs {
   SplitArgs a;            // part_o [2 ctas heads, G, D] and part_lse [2 ctas heads, G]: see
@@ -340,7 +368,8 @@ struct Int4DecodeArgs {
   int ctas;               // CTAs the batch is dealt to (by_row: not used)
   int groups;             // rows that the cut sees per sequence: KV heads, or eighths of them
   int heads;              // KV heads per row of the cut: 1, or 8 (a warp each)
-  bool by_row;            // one CTA per (sequence, KV head), no partial results
+  bool by_row;            // one cluster per (sequence, KV head), no partial results
+  int cluster;            // its CTAs (by_row), at most kInt4MaxCluster
   bool evict_first;       // what is read leaves L2 first
 };
 
@@ -621,6 +650,90 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
     if (!mbar_wait(bar + 8 * (i % kStages), (i / kStages) & 1, kWaitLimitNs)) raise_device_error(2u);
 }
 
+// A row that a cluster shares: each CTA merges its warps' states, one per warp, into
+// one at the start of its (drained) rings, and the entries of the result are dealt to
+// the CTAs, which read the states of all.  Two arrivals and a read of the neighbours'
+// shared memory take about 1 us where the partial results in device memory and the
+// second kernel take 4.4 (64/8 heads, D = 128: 1 x 2,048 tokens 7.9 us against 11.1
+// from graph replays; 5 x 3,001, 8/8, D = 64: 9.4 against 12.4).  A unit costs its warp
+// about 2 us, the same with fewer warps at work, so that a row gains from more CTAs
+// until each warp has one.
+template <int D, class L>
+__device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint8_t* smem, const Int4Piece* pieces,
+                                                   bool good, int b, int h, int lane) {
+  constexpr int kWarps = L::kInt4Warps, kChunks = D / 4;
+  const SplitArgs& a = p.a;
+  const unsigned held = __ballot_sync(0xffffffffu, lane < kWarps && pieces[2 * min(lane, kWarps - 1)].row >= 0);
+  float* own = reinterpret_cast<float*>(smem);         // as a warp's state, kAccStride apart
+  const int items = a.G * kChunks;
+  if (good) {
+    for (int c = threadIdx.x; c < items; c += kWarps * 32) {
+      const int hd = c / kChunks, d = (c % kChunks) * 4;
+      const float* states = reinterpret_cast<const float*>(smem + L::kFirstOffset);
+      float m[kWarps], M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        m[k] = (held >> k) & 1u ? states[k * L::kStateFloats + L::kM + hd] : -INFINITY;
+        M = fmaxf(M, m[k]);
+      }
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        if ((held >> k) & 1u) {
+          const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M);
+          const float4 v = *reinterpret_cast<const float4*>(states + k * L::kStateFloats + hd * L::kAccStride + d);
+          l += wt * states[k * L::kStateFloats + L::kL + hd];
+          o.x += wt * v.x;
+          o.y += wt * v.y;
+          o.z += wt * v.z;
+          o.w += wt * v.w;
+        }
+      *reinterpret_cast<float4*>(own + hd * L::kAccStride + d) = o;
+      if (d == 0) {
+        own[L::kM + hd] = M;
+        own[L::kL + hd] = l;
+      }
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  const int share = (items + p.cluster - 1) / p.cluster;
+  const int first = static_cast<int>(blockIdx.x % p.cluster) * share;
+  const uint32_t base = smem_u32(smem);
+  for (int c = first + threadIdx.x; good && c < min(first + share, items); c += kWarps * 32) {
+    const int hd = c / kChunks, d = (c % kChunks) * 4;
+    float m[kInt4MaxCluster], l[kInt4MaxCluster], M = -INFINITY, sum = 0.f;
+    float4 v[kInt4MaxCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kInt4MaxCluster; ++k)
+      if (k < p.cluster) {
+        const uint32_t at = cluster_address(base, k);
+        m[k] = cluster_load(at + 4 * (L::kM + hd));
+        l[k] = cluster_load(at + 4 * (L::kL + hd));
+        v[k] = cluster_load4(at + 4 * (hd * L::kAccStride + d));
+        M = fmaxf(M, m[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < kInt4MaxCluster; ++k)
+      if (k < p.cluster) {
+        const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M);
+        sum += wt * l[k];
+        o.x += wt * v[k].x;
+        o.y += wt * v[k].y;
+        o.z += wt * v[k].z;
+        o.w += wt * v[k].w;
+      }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t orow = static_cast<size_t>(b) * a.Hq + h * a.G + hd;
+    *reinterpret_cast<uint2*>(a.out + orow * D + d) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (d == 0 && a.lse) a.lse[orow] = (M + log2f(sum)) * 0.69314718055994530942f;
+  }
+  cluster_arrive();                                    // a CTA's memory stays until all have read it
+  cluster_wait();
+}
+
 // Decode attention over a 4-bit cache.  A row that lies within a warp's range is
 // finished by the warp, one within a CTA's by the CTA; of a row that goes over
 // the end of CTA c's range each CTA leaves one partial result (with eight heads at
@@ -719,12 +832,13 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
 
   if (p.by_row) {
     cur.b = blockIdx.y;
-    cur.h = blockIdx.x;
+    cur.h = blockIdx.x / p.cluster;
     cur.n = int4_length(a, cur.b);
     cur.units = (cur.n + kUnit - 1) / kUnit;
     cta_end = cur.units;
-    cur.u = cur.units * warp / kInt4Warps;
-    mine = cur.units * (warp + 1) / kInt4Warps - cur.u;
+    const int warps = kInt4Warps * p.cluster, at = static_cast<int>(blockIdx.x % p.cluster) * kInt4Warps + warp;
+    cur.u = static_cast<int>(static_cast<long long>(cur.units) * at / warps);
+    mine = static_cast<int>(static_cast<long long>(cur.units) * (at + 1) / warps) - cur.u;
   } else {
     uint32_t total = 0, rows = 0;
     for (int b = lane; b < B; b += 32) {
@@ -1123,7 +1237,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
 
   // ---- the row's end within the range.  Row g of m-block j of group h is entry
   // h D/2 + g D/16 + 2 j, row g + 8 the next one.
-  const bool whole = u_first == 0 && count == cur.units;
+  const bool whole = u_first == 0 && count == cur.units && p.cluster == 1;
   const bool is_first = done == 0;
   float* f = reinterpret_cast<float*>(is_first ? smem + L::kFirstOffset + warp * L::kStateFloats * 4 : ring);
   if (!whole && !is_first) __syncwarp();               // the ring is drained, and read by every lane
@@ -1210,13 +1324,18 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     for (int b = p.by_row ? blockIdx.y : blockIdx.x; b < B; b += p.by_row ? B : gridDim.x) {
       if ((p.by_row ? cur.n : int4_length(a, lens, b)) > 0) continue;
       const int rows = p.by_row ? a.G : a.Hq;
-      const size_t row = static_cast<size_t>(b) * a.Hq + (p.by_row ? blockIdx.x * a.G : 0);
+      const size_t row = static_cast<size_t>(b) * a.Hq + (p.by_row ? blockIdx.x / p.cluster * a.G : 0);
       for (int i = threadIdx.x; i < rows * D; i += kInt4Warps * 32) a.out[row * D + i] = __float2bfloat16_rn(0.f);
       if (a.lse)
         for (int i = threadIdx.x; i < rows; i += kInt4Warps * 32) a.lse[row + i] = -INFINITY;
     }
   }
   __syncthreads();
+  if (p.cluster > 1) {
+    // Without a token the zeros above are the result (written by every CTA alike).
+    if (cur.n > 0) int4_cluster_merge<D, L>(p, smem, pieces, *cta_error == 0, cur.b, cur.h, lane);
+    return;
+  }
   if (*cta_error) return;
 
   // ---- rows that several warps share, one after another.  Lane k of each warp

@@ -38,19 +38,27 @@ fd_status this_device(int* dev) {
 // Launches that may start while the previous kernel of the stream ends (every
 // kernel waits for it before its first read).
 template <class Kernel, class... Args>
-fd_status launch_chained(Kernel kernel, dim3 grid, int threads, size_t smem, fd_stream_t stream,
-                         const Args&... args) {
+fd_status launch_clusters(Kernel kernel, dim3 grid, int cluster, int threads, size_t smem, fd_stream_t stream,
+                          const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+template <class Kernel, class... Args>
+fd_status launch_chained(Kernel kernel, dim3 grid, int threads, size_t smem, fd_stream_t stream,
+                         const Args&... args) {
+  return launch_clusters(kernel, grid, 1, threads, smem, stream, args...);
 }
 
 // Tensor maps of a 4-bit cache, {byte, head, row, plane}: the codes of K and of
@@ -128,7 +136,8 @@ fd_status launch_split_int4(const Int4Maps& m, const fd::Int4DecodeArgs& a, dim3
       return FD_ERR_CUDA;
     attr_ctx[dev].store(ctx);
   }
-  return launch_chained(kern, grid, (SH::WARPS + fd::kInt4CopyWarps) * 32, L::kDynamicBytes, s, m.k, m.v, m.p, a);
+  return launch_clusters(kern, grid, a.cluster, (SH::WARPS + fd::kInt4CopyWarps) * 32, L::kDynamicBytes, s,
+                         m.k, m.v, m.p, a);
 }
 
 // Rows of many parts (on average) are merged by four warps per query head, which
@@ -299,7 +308,8 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = a.part_o + static_cast<size_t>(2) * d.ctas * d.heads * a.G * p->D;
   }
-  const dim3 grid = d.by_row ? dim3(static_cast<unsigned>(p->Hkv), static_cast<unsigned>(p->B))
+  d.cluster = d.by_row ? int4_cluster(sms, rows, p->max_len) : 1;
+  const dim3 grid = d.by_row ? dim3(static_cast<unsigned>(p->Hkv * d.cluster), static_cast<unsigned>(p->B))
                              : dim3(static_cast<unsigned>(d.ctas));
   fd_status r;
   if (p->D == 128)

@@ -232,6 +232,30 @@ def test_eight_heads_of_many_sequences(B, most):
         check(*decode(c, S), ref, f"B={B} S={S}")
 
 
+@pytest.mark.parametrize("B,most,G,D,bs,layout", [
+    (15, 4096, 4, 128, 0, HND),      # 8 CTAs to a row
+    (15, 3400, 16, 64, 8, NHD),      # 7
+    (22, 4096, 1, 64, 16, HND),      # 6
+    (26, 4100, 8, 128, 0, NHD),      # 5
+    (33, 1990, 2, 128, 256, HND),    # 4
+    (45, 1300, 16, 128, 32, HND),    # 3
+    (74, 1000, 8, 64, 64, NHD)])     # 2
+def test_rows_that_a_cluster_shares(B, most, G, D, bs, layout):
+    """num_splits = 1 and few rows: lengths that leave CTAs and warps of a cluster
+    without a token, none, and one; the result does not depend on the other rows."""
+    t = torch()
+    lens = np.random.default_rng(B).integers(0, most + 1, B).tolist()
+    lens[:10] = [most, 0, 1, 63, 64, 65, 512, 513, most - 1, 0]
+    most_rows = most if bs == 0 else -(-most // bs) * bs
+    c = Cache(lens, G, 1, D, most_rows, seed=950 + B, block_size=bs, layout=layout).on_device()
+    out, lse = decode(c, 1)
+    check(out, lse, c.oracle(), f"B={B}")
+    c.dl = c.dl.clone()
+    c.dl[0], c.dl[3:] = 7, 5
+    again, _ = decode(c, 1)
+    assert t.equal(again[1:3], out[1:3])
+
+
 def test_seqlens_are_clamped_and_optional():
     c = Cache([90, 90], 8, 1, 64, 90, seed=9).on_device()
     ref = c.oracle()

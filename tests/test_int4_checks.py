@@ -130,7 +130,7 @@ def test_page_refusals():
 def test_planner_takes_4_bit_caches():
     """The least count whose workspace serves a CTA on each of the 148 SMs (two
     partial results each; two for each of eight KV heads with Hkv a multiple of 8
-    and five such rows); short histories of few rows keep one CTA per row."""
+    and five such rows); short histories and few rows keep one cluster per row."""
     def plan(B, Hkv, L, lens=None, D=128):
         return fd.fd_plan_problem(148, fd.make_problem(B, 8 * Hkv, Hkv, D, L, kv_dtype=fd.FD_KV_INT4),
                                   lens)
@@ -141,8 +141,8 @@ def test_planner_takes_4_bit_caches():
         assert B * Hkv * S // (2 * heads) >= 148
         assert S == 2 or B * Hkv * (S - 1) // (2 * heads) < 148
     assert plan(1, 8, 0) == plan(1, 8, 1) == plan(1, 8, 512) == plan(18, 8, 512, D=64) == 1
-    assert plan(1, 8, 1536) == 1 and plan(1, 8, 1537) > 1 and plan(19, 8, 512) > 1
-    assert plan(2, 8, 65536, [1536, 7]) == 1 and plan(2, 8, 65536, [1537, 7]) > 1
+    assert plan(1, 8, 12288) == 1 and plan(1, 8, 12289) > 1 and plan(19, 8, 512) > 1
+    assert plan(2, 8, 65536, [6144, 7]) == 1 and plan(2, 8, 65536, [6145, 7]) > 1
     assert plan(18, 8, 4096) == 1 and plan(18, 8, 65536) > 1
     assert plan(18, 8, 4096, [4096] + 17 * [7]) > 1
     assert plan(2, 8, 65536, [-4, 0]) == 1

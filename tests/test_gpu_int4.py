@@ -439,6 +439,38 @@ def test_capture_and_replay_with_other_lengths():
         check(out, lse, c.oracle(), f"replay {lens}")
 
 
+def test_clusters_captured_and_on_two_streams():
+    """num_splits = 1 with a cluster per row: one graph replayed with other lengths
+    (rows that leave CTAs of the cluster idle among them), while a second stream runs
+    the same rows; nothing is shared between the two but the inputs."""
+    t = torch()
+    c = Cache([3000, 3000, 2999, 2049], 8, 2, 128, 3000, seed=735).on_device()
+    outs = [t.empty_like(c.dq) for _ in range(2)]
+    lses = [t.empty((c.B, c.Hq), device="cuda") for _ in range(2)]
+    side = t.cuda.Stream()
+    run = lambda i, s=None: fd.decode_int4(c.dq, c.dk, c.dv, c.dp, c.dl, scale=c.scale,  # noqa: E731
+                                           num_splits=1, out=outs[i], lse=lses[i], stream=s)
+    t.cuda.synchronize()
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        run(0)
+    for lens in ([3000, 130, 0, 2049], [1, 0, 0, 64], [0, 0, 0, 0], [65, 3000, 2999, 513]):
+        c.dl.copy_(t.tensor(lens, dtype=t.int32))
+        c.lens = lens
+        for x in outs:
+            x.fill_(7.0)
+        t.cuda.synchronize()
+        for _ in range(20):
+            g.replay()
+            run(1, side)
+        t.cuda.synchronize()
+        ref = c.oracle()
+        for i in range(2):
+            check(outs[i], lses[i], ref, f"{lens} {i}")
+        assert t.equal(outs[0], outs[1]) and t.equal(lses[0], lses[1])
+    assert fd.fd_check_device_error() == fd.FD_OK
+
+
 def test_slots_past_32_bits_of_bytes():
     """Rows whose byte offset does not fit 32 bits: a contiguous cache of 4.8 GB
     of codes a tensor, of which the last rows are used."""

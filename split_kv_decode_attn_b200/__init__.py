@@ -156,12 +156,19 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr() or None
 
 
+_raw_stream = _device = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _raw_stream, _device
     if stream is None:
         # The raw handle: building torch's Stream object takes 3.2 us, half of a
-        # small call.
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        # small call, and the checks of torch.cuda.current_device() are made once.
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_device()
+            _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        return _raw_stream(_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

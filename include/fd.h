@@ -435,7 +435,8 @@ FD_API fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void*
  *               between calls.
  * Scores and sums are taken in fp32. A softmax weight enters the product with V's
  * codes as weight * scale in f16 (11 significant bits), relative to a power of
- * two above the largest V scale that its warp has seen. The result of a call is
+ * two above the largest V scale (and 2^-64 of the largest V bias) that its warp has
+ * seen. V may be of any finite size: no sum on the way is larger than the result. The result of a call is
  * the same bits every time; how a sequence's sum is split over CTAs, and with it
  * the last bits of its result, depends on the other sequences' lengths when
  * num_splits is above 1, but not on the order of the cache's dimensions or pages. */

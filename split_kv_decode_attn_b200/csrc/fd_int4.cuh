@@ -290,6 +290,13 @@ struct Int4Shape {
 };
 constexpr float kRescaleLog2 = 8.f;   // a score may pass the reference by 2^8 ...
 constexpr float kWeightLog2 = 7.f;    // ... whose own weight is 2^7
+constexpr float kBiasRoom = 0x1p-64f;  // a bias of V may pass R by 2^64 (see P V below)
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 
 // 4-D tile load: {byte, head, row, plane}.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, uint32_t bar,
@@ -360,6 +367,7 @@ __device__ __forceinline__ T smem_at(const uint8_t* p) {
 }
 
 constexpr int kInt4MaxCluster = 8;    // the portable limit
+constexpr int kInt4MaxCtas = 256;     // that the batch is dealt to, a power of two
 
 struct Int4DecodeArgs {
   SplitArgs a;            // part_o [2 ctas heads, G, D] and part_lse [2 ctas heads, G]: see
@@ -511,7 +519,7 @@ struct Int4Smem {
   static constexpr int kStageBytes = 2 * kCodeBytes + kUnit * 16;
   static constexpr int kWarpBytes = kInt4Stages * kStageBytes;
   // V's part of a unit's records, unpacked: vs0 / R, vs1 / R in fp32 per token,
-  // then vb0, vb1 in bf16.  (K's part, in fp32, takes the records' place.)
+  // then vb0 / R, vb1 / R in bf16.  (K's part, in fp32, takes the records' place.)
   static constexpr int kVRecOffset = kInt4Warps * kWarpBytes;
   static constexpr int kVRecBytes = kUnit * 12;
   // A softmax state (floats): [column][kAccStride] outputs, the columns'
@@ -756,10 +764,13 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
 //   t = ks0 S0 + ks1 S1 + (kb0 - 8 ks0) sum_0(q) + (kb1 - 8 ks1) sum_1(q),
 // so that no scale touches an entry.
 // P V.  O^T += c^T w on the same MMAs, w = f16(p vs / R) with R a power of
-// two above every vs the warp has seen (f16's 11 bits; p vs of any size fits).
-// One more MMA per group sums 8 w as the tensor core sees it, which the end
-// takes off: c - 8, with no rounding of w left in it.  The biases' part
-// sum_j p_j vb_j is summed in fp32 beside it.
+// two above every |vs| (and 2^-64 of every |vb|) that the warp has seen: f16's 11
+// bits for V of any size.  One more MMA per group sums 8 w as the tensor core sees
+// it, which the end takes off: c - 8, with no rounding of w left in it.  The
+// biases' part sum_j p_j vb_j / R is summed in fp32 beside it; the factor R comes
+// in once the row's sum is divided by that of the weights, so that nothing on the
+// way is larger than the result.  (1 x 65,536 tokens at 64/8 heads 25.2 us, 25.0
+// with the plain sums, which overflowed from |V| = 1e31 on.)
 // The running maximum is only moved when a score passes it by 2^8 (a vote per
 // unit in place of shuffles), and the weights are 2^7 p, so that they use f16's
 // range: up to 2^15, and down to 2^-31 of the largest before one is lost.
@@ -1017,17 +1028,22 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     // instructions per 32 tokens.
     {
       uint4 rec[kUnit / 32];
-      float vtop[2] = {0.f, 0.f};
+      float vtop[2] = {0.f, 0.f}, btop[2] = {0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < kUnit / 32; ++x) {
         rec[x] = smem_at<uint4>(st + L::kP + (32 * x + lane) * 16);
         if (32 * x + lane >= valid) rec[x] = make_uint4(0u, 0u, 0u, 0u);
         vtop[0] = fmaxf(vtop[0], fabsf(bf16_lo(rec[x].z)));
         vtop[1] = fmaxf(vtop[1], fabsf(bf16_lo(rec[x].w)));
+        // The bias is the high half; as fp32 the word is at most a bf16 step larger.
+        btop[0] = fmaxf(btop[0], fabsf(__uint_as_float(rec[x].z)));
+        btop[1] = fmaxf(btop[1], fabsf(__uint_as_float(rec[x].w)));
       }
-      if (__any_sync(0xffffffffu, vtop[0] * inv_r[0] > 1.f || vtop[1] * inv_r[1] > 1.f)) {
+      if (__any_sync(0xffffffffu, fmaxf(fmaxf(vtop[0] * inv_r[0], vtop[1] * inv_r[1]),
+                                        fmaxf(btop[0] * (inv_r[0] * kBiasRoom), btop[1] * (inv_r[1] * kBiasRoom))) > 1.f)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          vtop[h] = fmaxf(vtop[h], btop[h] * kBiasRoom);
 #pragma unroll
           for (int off = 1; off < 32; off <<= 1) vtop[h] = fmaxf(vtop[h], __shfl_xor_sync(0xffffffffu, vtop[h], off));
           if (vtop[h] * inv_r[h] > 1.f) {
@@ -1038,6 +1054,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
             if (i == 0) continue;                      // nothing is summed yet
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
+              bias[nb][h][0] *= keep;
+              bias[nb][h][1] *= keep;
               eight[nb][2 * h] *= keep;
               eight[nb][2 * h + 1] *= keep;
 #pragma unroll
@@ -1048,6 +1066,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
           }
         }
       }
+      const uint32_t inv_r2 = __byte_perm(__float_as_uint(inv_r[0]), __float_as_uint(inv_r[1]), 0x7632);
 #pragma unroll
       for (int x = 0; x < kUnit / 32; ++x) {
         const float ks0 = bf16_lo(rec[x].x), ks1 = bf16_lo(rec[x].y);
@@ -1056,7 +1075,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
             make_float4(ks0, fmaf(-8.f, ks0, bf16_hi(rec[x].x)), ks1, fmaf(-8.f, ks1, bf16_hi(rec[x].y)));
         *reinterpret_cast<float2*>(v_recs + at * 8) =
             make_float2(bf16_lo(rec[x].z) * inv_r[0], bf16_lo(rec[x].w) * inv_r[1]);
-        *reinterpret_cast<uint32_t*>(v_recs + kUnit * 8 + at * 4) = __byte_perm(rec[x].z, rec[x].w, 0x7632);
+        *reinterpret_cast<uint32_t*>(v_recs + kUnit * 8 + at * 4) =
+            mul_bf16x2(__byte_perm(rec[x].z, rec[x].w, 0x7632), inv_r2);
       }
       __syncwarp();
     }
@@ -1256,19 +1276,24 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       const int col = nb * 8 + 2 * t4 + c;
       const size_t orow = static_cast<size_t>(cur.b) * a.Hq + (cur.h * p.heads + head) * a.G + col;
       const size_t prow = part * a.G + col;
-      const float inv = l_run[nb][c] == 0.f ? 0.f : 1.f / l_run[nb][c];
+      // A result is divided by the sum of weights l, a state by a power of two that
+      // leaves l in [2^-8, 2^-7): what 8 warps and 8 CTAs of a cluster have adds up to
+      // less than the largest |V| then.
+      const bool state = !whole && !alone;
+      const uint32_t le = __float_as_uint(l_run[nb][c]) >> 23;
+      const float inv = state ? __uint_as_float((246u - le) << 23) : l_run[nb][c] == 0.f ? 0.f : 1.f / l_run[nb][c];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float r = 1.f / inv_r[h], r0 = r * 0x1p24f, r1 = r * 0x1p20f;
+        const float r = 1.f / inv_r[h];
         const float w8 = eight[nb][2 * h + c];
         const int d = h * (D / 2) + g * (D / 16);
         float o[2 * MB];
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          o[2 * j] = fmaf(acc[nb][h][j][c] - w8, r0, bias[nb][h][c]);
-          o[2 * j + 1] = fmaf(acc[nb][h][j][c + 2] - 16.f * w8, r1, bias[nb][h][c]);
+          o[2 * j] = fmaf(acc[nb][h][j][c] - w8, 0x1p24f, bias[nb][h][c]) * inv * r;
+          o[2 * j + 1] = fmaf(acc[nb][h][j][c + 2] - 16.f * w8, 0x1p20f, bias[nb][h][c]) * inv * r;
         }
-        if (!whole && !alone) {
+        if (state) {
 #pragma unroll
           for (int j = 0; j < 2 * MB; j += 4)
             *reinterpret_cast<float4*>(f + col * L::kAccStride + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
@@ -1276,12 +1301,11 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
           if (col < a.G)
 #pragma unroll
             for (int j = 0; j < 2 * MB; j += 4)
-              *reinterpret_cast<float4*>(a.part_o + prow * D + d + j) =
-                  make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
+              *reinterpret_cast<float4*>(a.part_o + prow * D + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         } else if (col < a.G) {
           uint32_t w[MB];
 #pragma unroll
-          for (int j = 0; j < MB; ++j) w[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+          for (int j = 0; j < MB; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
           if constexpr (MB == 4)
             *reinterpret_cast<uint4*>(a.out + orow * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
           else
@@ -1290,9 +1314,9 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       }
       if (g == 0) {
         const float lse = (ref[nb][c] + log2f(l_run[nb][c])) * 0.69314718055994530942f;
-        if (!whole && !alone) {
-          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
-          f[L::kL + col] = l_run[nb][c];
+        if (state) {
+          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c] + static_cast<float>(static_cast<int>(le) - 119);
+          f[L::kL + col] = l_run[nb][c] * inv;
         } else if (!whole) {
           if (col < a.G) a.part_lse[prow] = lse;
         } else if (col < a.G && a.lse) {
@@ -1407,6 +1431,7 @@ template <int D, int U, int SHARE, int BATCH>
 __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel(const Int4DecodeArgs p) {
   constexpr int VPL = D / 32;
   constexpr float kLog2e = 1.4426950408889634074f;
+  constexpr float kPart = 1.f / kInt4MaxCtas;          // of a weight: sums of finite parts stay finite
   __shared__ int lens[kInt4Lens];
   const SplitArgs& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -1500,7 +1525,7 @@ __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
       if (s + j * SHARE < parts) {
-        const float wt = mx == -INFINITY ? 0.f : ex2((lb[j] - mx) * kLog2e);
+        const float wt = mx == -INFINITY ? 0.f : ex2((lb[j] - mx) * kLog2e) * kPart;
         W += wt;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) acc[i] += wt * ob[j][i];
@@ -1525,7 +1550,7 @@ __global__ void __launch_bounds__(kInt4CombineWarps * 32) fd_combine_int4_kernel
         make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(a.out + r * D + lane * 2) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (a.lse && lane == 0) a.lse[r] = mx + logf(W);
+  if (a.lse && lane == 0) a.lse[r] = mx + logf(W * kInt4MaxCtas);
 }
 
 }  // namespace fd

@@ -297,6 +297,7 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   d.B = p->B;
   int sms = 0;
   if (device_sms(dev, &sms) != FD_OK) return FD_ERR_CUDA;
+  sms = std::min(sms, fd::kInt4MaxCtas);
   const long long rows = static_cast<long long>(p->B) * p->Hkv;
   if (rows * ((p->max_len + unit - 1LL) / unit + 1) > 0x7fffffffLL) return FD_ERR_INVALID_ARGUMENT;
   d.by_row = num_splits == 1;

@@ -1,0 +1,93 @@
+"""fd_decode_int4 over the whole range of bf16: rows that fd_append_int4 takes and
+fd_expand_int4 gives back finite, up to the largest, against the fp64 oracle and
+its derived bounds.  (All scalings are by powers of two, so the bounds of the
+ordinary sizes hold unchanged.)"""
+import numpy as np
+import pytest
+
+import split_kv_decode_attn_b200 as fd
+from split_kv_decode_attn_b200 import workloads as wl
+
+from int4test import HND, NHD, Cache, check, rows, torch
+
+pytestmark = pytest.mark.gpu
+
+LARGEST = 3e38      # of a V entry: the values of its codes stay below the largest bf16
+
+
+@pytest.fixture(autouse=True)
+def _gpu(cuda_device):
+    yield
+    assert fd.fd_check_device_error() == fd.FD_OK
+
+
+def decode(c, S=None):
+    out, lse = fd.decode_int4(c.dq, c.dk, c.dv, c.dp, c.dl, c.dt, kv_layout=c.layout,
+                              max_len=c.max_len, scale=c.scale, num_splits=S)
+    torch().cuda.synchronize()
+    return out, lse
+
+
+def large(seed, shape, size):
+    """V rows of one size, cut off at the largest."""
+    v = wl.bf16_bits_to_f64(rows(seed, shape)) * size
+    return wl.f64_to_bf16_bits(np.clip(v, -LARGEST, LARGEST))
+
+
+# ------------------------------------------------------------------------ V
+
+@pytest.mark.parametrize("size", [2e31, 1e33, 1e37, LARGEST])
+@pytest.mark.parametrize("G,D", [(8, 128), (16, 128), (1, 64)])
+def test_large_values(size, G, D):
+    """Clusters, one CTA, ranges of CTAs and of warps, one head or eight at a time."""
+    for B, n, Hkv in ((1, 200, 2), (3, 1500, 1), (5, 700, 8)):
+        lens = ([n, 1, n - 65, 0, 64] * B)[:B]
+        c = Cache(lens, G * Hkv, Hkv, D, n, seed=1000 + G + B,
+                  v=large(21, (B, Hkv, n, D), size)).on_device()
+        ref = c.oracle()
+        assert np.isfinite(ref[0]).all() and np.abs(ref[0]).max() < LARGEST * 1.01
+        for S in (None, 1, 2, 3, 40, 400):
+            check(*decode(c, S), ref, f"size={size} G={G} D={D} B={B} S={S}")
+
+
+@pytest.mark.parametrize("value", [1e34, LARGEST, -LARGEST])
+@pytest.mark.parametrize("n", [3, 6000])
+def test_large_constant_values_of_equal_weight(value, n):
+    """Constant rows have scale 0 and all of their size in the bias; with q = 0 every
+    token has the same weight, and the result is the value itself."""
+    t = torch()
+    v = wl.f64_to_bf16_bits(np.full((2, 8, n, 64), value))
+    c = Cache([n, max(n - 70, 1)], 16, 8, 64, n, seed=1100, v=v)
+    c.q[:] = 0
+    c.on_device()
+    ref = c.oracle()
+    for S in (None, 1, 2, 30, 400):
+        out, lse = decode(c, S)
+        check(out, lse, ref, f"value={value} n={n} S={S}")
+        assert t.equal(out, t.full_like(out, value))
+
+
+@pytest.mark.parametrize("layout,bs", [(HND, 0), (NHD, 16)])
+def test_values_of_every_size_along_one_history(layout, bs):
+    """Sizes from 1 to the largest in one history, in random order, rising and
+    falling: the weights' reference moves by up to 2^120 and the biases with it."""
+    n = 20000
+    r = np.random.default_rng(7)
+    for gain in (r.uniform(0, 120, n), np.linspace(0, 120, n), np.linspace(120, 0, n)):
+        v = wl.bf16_bits_to_f64(rows(31, (1, 1, n, 128)))
+        v = np.clip(v * 2.0 ** np.round(gain)[:, None], -LARGEST, LARGEST)
+        c = Cache([n], 8, 1, 128, n, seed=1200, block_size=bs, layout=layout,
+                  v=wl.f64_to_bf16_bits(v)).on_device()
+        ref = c.oracle()
+        for S in (1, 2, 37, 300):
+            check(*decode(c, S), ref, f"S={S}")
+
+
+@pytest.mark.parametrize("size", [1e-38, 1e-34])
+def test_smallest_values(size):
+    """Down to bf16's subnormals, whose step (2^-133) replaces the relative bound."""
+    v = wl.f64_to_bf16_bits(wl.bf16_bits_to_f64(rows(41, (2, 2, 900, 64))) * size)
+    c = Cache([900, 65], 8, 2, 64, 900, seed=1300, v=v).on_device()
+    o, lse, tol, ltol = c.oracle()
+    for S in (None, 1, 2, 20):
+        check(*decode(c, S), (o, lse, tol + 2.0 ** -133, ltol), f"size={size} S={S}")

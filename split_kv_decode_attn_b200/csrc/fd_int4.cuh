@@ -292,6 +292,9 @@ constexpr float kRescaleLog2 = 8.f;   // a score may pass the reference by 2^8 .
 constexpr float kWeightLog2 = 7.f;    // ... whose own weight is 2^7
 constexpr float kBiasRoom = 0x1p-64f;  // a bias of V may pass R by 2^64 (see P V below)
 
+// 1 / x of a power of two within 2^+-126.
+__device__ __forceinline__ float power_inverse(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
@@ -522,15 +525,16 @@ struct Int4Smem {
   // then vb0 / R, vb1 / R in bf16.  (K's part, in fp32, takes the records' place.)
   static constexpr int kVRecOffset = kInt4Warps * kWarpBytes;
   static constexpr int kVRecBytes = kUnit * 12;
-  // A softmax state (floats): [column][kAccStride] outputs, the columns'
-  // references and sums.  A warp leaves up to two: that of the row its range
+  // A softmax state (floats): [column][kAccStride] outputs over R, the columns'
+  // references and sums, R of both groups.  A warp leaves up to two: that of the row its range
   // begins in, in a place of its own, and that of the row its range ends in, over
   // its drained ring.
   static constexpr int kNcol = NB * 8;
   static constexpr int kAccStride = D + 4;
   static constexpr int kM = kNcol * kAccStride;
   static constexpr int kL = kM + kNcol;
-  static constexpr int kStateFloats = kL + kNcol;
+  static constexpr int kR = kL + kNcol;
+  static constexpr int kStateFloats = kR + 4;
   static_assert(kStateFloats * 4 <= kWarpBytes, "the state of a warp fits its ring");
   static constexpr int kFirstOffset = kVRecOffset + kInt4Warps * kVRecBytes;
   static constexpr int kRowOffset = kFirstOffset + kInt4Warps * kStateFloats * 4;   // Int4Piece[2 warps]
@@ -677,31 +681,36 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
   if (good) {
     for (int c = threadIdx.x; c < items; c += kWarps * 32) {
       const int hd = c / kChunks, d = (c % kChunks) * 4;
+      const int group = d / (D / 2);
       const float* states = reinterpret_cast<const float*>(smem + L::kFirstOffset);
-      float m[kWarps], M = -INFINITY;
+      float m[kWarps], r[kWarps], M = -INFINITY, R = 0x1p-126f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         m[k] = (held >> k) & 1u ? states[k * L::kStateFloats + L::kM + hd] : -INFINITY;
+        r[k] = (held >> k) & 1u ? states[k * L::kStateFloats + L::kR + group] : 0.f;
         M = fmaxf(M, m[k]);
+        R = fmaxf(R, r[k]);
       }
+      const float inv_r = power_inverse(R);
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k)
         if ((held >> k) & 1u) {
-          const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M);
+          const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M), wr = wt * (r[k] * inv_r);
           const float4 v = *reinterpret_cast<const float4*>(states + k * L::kStateFloats + hd * L::kAccStride + d);
           l += wt * states[k * L::kStateFloats + L::kL + hd];
-          o.x += wt * v.x;
-          o.y += wt * v.y;
-          o.z += wt * v.z;
-          o.w += wt * v.w;
+          o.x += wr * v.x;
+          o.y += wr * v.y;
+          o.z += wr * v.z;
+          o.w += wr * v.w;
         }
       *reinterpret_cast<float4*>(own + hd * L::kAccStride + d) = o;
       if (d == 0) {
         own[L::kM + hd] = M;
         own[L::kL + hd] = l;
       }
+      if (hd == 0 && d % (D / 2) == 0) own[L::kR + group] = R;
     }
   }
   cluster_arrive();
@@ -711,7 +720,8 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
   const uint32_t base = smem_u32(smem);
   for (int c = first + threadIdx.x; good && c < min(first + share, items); c += kWarps * 32) {
     const int hd = c / kChunks, d = (c % kChunks) * 4;
-    float m[kInt4MaxCluster], l[kInt4MaxCluster], M = -INFINITY, sum = 0.f;
+    const int group = d / (D / 2);
+    float m[kInt4MaxCluster], l[kInt4MaxCluster], r[kInt4MaxCluster], M = -INFINITY, R = 0x1p-126f, sum = 0.f;
     float4 v[kInt4MaxCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kInt4MaxCluster; ++k)
@@ -719,23 +729,26 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
         const uint32_t at = cluster_address(base, k);
         m[k] = cluster_load(at + 4 * (L::kM + hd));
         l[k] = cluster_load(at + 4 * (L::kL + hd));
+        r[k] = cluster_load(at + 4 * (L::kR + group));
         v[k] = cluster_load4(at + 4 * (hd * L::kAccStride + d));
         M = fmaxf(M, m[k]);
+        R = fmaxf(R, r[k]);
       }
+    const float inv_r = power_inverse(R);
 #pragma unroll
     for (int k = 0; k < kInt4MaxCluster; ++k)
       if (k < p.cluster) {
-        const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M);
+        const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M), wr = wt * (r[k] * inv_r);
         sum += wt * l[k];
-        o.x += wt * v[k].x;
-        o.y += wt * v[k].y;
-        o.z += wt * v[k].z;
-        o.w += wt * v[k].w;
+        o.x += wr * v[k].x;
+        o.y += wr * v[k].y;
+        o.z += wr * v[k].z;
+        o.w += wr * v[k].w;
       }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const size_t orow = static_cast<size_t>(b) * a.Hq + h * a.G + hd;
     *reinterpret_cast<uint2*>(a.out + orow * D + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        make_uint2(pack_bf16x2(o.x * inv * R, o.y * inv * R), pack_bf16x2(o.z * inv * R, o.w * inv * R));
     if (d == 0 && a.lse) a.lse[orow] = (M + log2f(sum)) * 0.69314718055994530942f;
   }
   cluster_arrive();                                    // a CTA's memory stays until all have read it
@@ -769,7 +782,7 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
 // it, which the end takes off: c - 8, with no rounding of w left in it.  The
 // biases' part sum_j p_j vb_j / R is summed in fp32 beside it; the factor R comes
 // in once the row's sum is divided by that of the weights, so that nothing on the
-// way is larger than the result.  (1 x 65,536 tokens at 64/8 heads 25.2 us, 25.0
+// way is larger than the result.  (1 x 65,536 tokens at 64/8 heads 25.3 us, 25.0
 // with the plain sums, which overflowed from |V| = 1e31 on.)
 // The running maximum is only moved when a score passes it by 2^8 (a vote per
 // unit in place of shuffles), and the weights are 2^7 p, so that they use f16's
@@ -1276,22 +1289,18 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       const int col = nb * 8 + 2 * t4 + c;
       const size_t orow = static_cast<size_t>(cur.b) * a.Hq + (cur.h * p.heads + head) * a.G + col;
       const size_t prow = part * a.G + col;
-      // A result is divided by the sum of weights l, a state by a power of two that
-      // leaves l in [2^-8, 2^-7): what 8 warps and 8 CTAs of a cluster have adds up to
-      // less than the largest |V| then.
       const bool state = !whole && !alone;
-      const uint32_t le = __float_as_uint(l_run[nb][c]) >> 23;
-      const float inv = state ? __uint_as_float((246u - le) << 23) : l_run[nb][c] == 0.f ? 0.f : 1.f / l_run[nb][c];
+      const float inv = l_run[nb][c] == 0.f ? 0.f : 1.f / l_run[nb][c];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float r = 1.f / inv_r[h];
+        const float r = power_inverse(inv_r[h]);
         const float w8 = eight[nb][2 * h + c];
         const int d = h * (D / 2) + g * (D / 16);
         float o[2 * MB];
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          o[2 * j] = fmaf(acc[nb][h][j][c] - w8, 0x1p24f, bias[nb][h][c]) * inv * r;
-          o[2 * j + 1] = fmaf(acc[nb][h][j][c + 2] - 16.f * w8, 0x1p20f, bias[nb][h][c]) * inv * r;
+          o[2 * j] = fmaf(acc[nb][h][j][c] - w8, 0x1p24f, bias[nb][h][c]);
+          o[2 * j + 1] = fmaf(acc[nb][h][j][c + 2] - 16.f * w8, 0x1p20f, bias[nb][h][c]);
         }
         if (state) {
 #pragma unroll
@@ -1301,11 +1310,12 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
           if (col < a.G)
 #pragma unroll
             for (int j = 0; j < 2 * MB; j += 4)
-              *reinterpret_cast<float4*>(a.part_o + prow * D + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              *reinterpret_cast<float4*>(a.part_o + prow * D + d + j) =
+                  make_float4(o[j] * inv * r, o[j + 1] * inv * r, o[j + 2] * inv * r, o[j + 3] * inv * r);
         } else if (col < a.G) {
           uint32_t w[MB];
 #pragma unroll
-          for (int j = 0; j < MB; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+          for (int j = 0; j < MB; ++j) w[j] = pack_bf16x2(o[2 * j] * inv * r, o[2 * j + 1] * inv * r);
           if constexpr (MB == 4)
             *reinterpret_cast<uint4*>(a.out + orow * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
           else
@@ -1315,8 +1325,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       if (g == 0) {
         const float lse = (ref[nb][c] + log2f(l_run[nb][c])) * 0.69314718055994530942f;
         if (state) {
-          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c] + static_cast<float>(static_cast<int>(le) - 119);
-          f[L::kL + col] = l_run[nb][c] * inv;
+          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
+          f[L::kL + col] = l_run[nb][c];
         } else if (!whole) {
           if (col < a.G) a.part_lse[prow] = lse;
         } else if (col < a.G && a.lse) {
@@ -1329,6 +1339,8 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     pc.row = static_cast<long long>(cur.b) * a.Hkv + cur.h;
     pc.begin = row_begin;
     pc.units = cur.units;
+    f[L::kR] = power_inverse(inv_r[0]);
+    f[L::kR + 1] = power_inverse(inv_r[1]);
   }
   done += count;
   if (done < mine) {
@@ -1379,41 +1391,48 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     constexpr int kChunks = D / 4;
     for (int c = threadIdx.x; c < a.G * kChunks; c += kInt4Warps * 32) {
       const int hd = c / kChunks, d = (c % kChunks) * 4;
+      const int group = d / (D / 2);
       const float* states = reinterpret_cast<const float*>(smem);
-      float m[kPieces], M = -INFINITY;
+      float m[kPieces], r[kPieces], M = -INFINITY, R = 0x1p-126f;
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int at = (k & 1) ? (k >> 1) * (L::kWarpBytes / 4) : L::kFirstOffset / 4 + (k >> 1) * L::kStateFloats;
         m[k] = (held >> k) & 1u ? states[at + L::kM + hd] : -INFINITY;
+        r[k] = (held >> k) & 1u ? states[at + L::kR + group] : 0.f;
         M = fmaxf(M, m[k]);
+        R = fmaxf(R, r[k]);
       }
+      const float inv_r = power_inverse(R);
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int at = (k & 1) ? (k >> 1) * (L::kWarpBytes / 4) : L::kFirstOffset / 4 + (k >> 1) * L::kStateFloats;
         if ((held >> k) & 1u) {
-          const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M);
+          const float wt = M == -INFINITY ? 0.f : ex2(m[k] - M), wr = wt * (r[k] * inv_r);
           const float4 v = *reinterpret_cast<const float4*>(states + at + hd * L::kAccStride + d);
           l += wt * states[at + L::kL + hd];
-          o.x += wt * v.x;
-          o.y += wt * v.y;
-          o.z += wt * v.z;
-          o.w += wt * v.w;
+          o.x += wr * v.x;
+          o.y += wr * v.y;
+          o.z += wr * v.z;
+          o.w += wr * v.w;
         }
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
+      o.x = o.x * inv * R;
+      o.y = o.y * inv * R;
+      o.z = o.z * inv * R;
+      o.w = o.w * inv * R;
       const float lse = (M + log2f(l)) * 0.69314718055994530942f;
       if (whole) {
         // Rows are numbered b Hkv + h, queries b Hq + h G + head.
         const size_t orow = static_cast<size_t>(row) * a.G + hd;
         *reinterpret_cast<uint2*>(a.out + orow * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         if (d == 0 && a.lse) a.lse[orow] = lse;
       } else {
         const size_t prow = static_cast<size_t>(slot) * a.G + hd;
-        *reinterpret_cast<float4*>(a.part_o + prow * D + d) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        *reinterpret_cast<float4*>(a.part_o + prow * D + d) = o;
         if (d == 0) a.part_lse[prow] = lse;
       }
     }

@@ -91,3 +91,23 @@ def test_smallest_values(size):
     o, lse, tol, ltol = c.oracle()
     for S in (None, 1, 2, 20):
         check(*decode(c, S), (o, lse, tol + 2.0 ** -133, ltol), f"size={size} S={S}")
+
+
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 24, 2.0 ** 26])
+def test_equal_scores_of_any_size_are_merged_alike(size):
+    """One warp's 64 tokens and another's single one, all with the same score: the mean
+    of V.  A reference of 2^24 and more has no room for a change of it by less than 2."""
+    for D, G in ((128, 4), (64, 16)):
+        for n in (65, 1000, 3000):
+            k = np.ones((1, 1, n, D))
+            k[..., 1::2] = -1.0
+            c = Cache([n], G, 1, D, n, seed=1250, k=wl.f64_to_bf16_bits(k))
+            c.q = wl.f64_to_bf16_bits(np.tile(np.where(np.arange(D) % 2, -1.0, 1.0), (1, G, 1)) * size / D / c.scale)
+            c.on_device()
+            o = c.oracle()[0]
+            out, lse = decode(c, 1)
+            got = wl.bf16_bits_to_f64(out.view(torch().int16).cpu().numpy().view(np.uint16))
+            # 2^-8 of the result, 2^-11 (a weight in f16) of scale * (code - 8), which is at
+            # most 8 / 15 (1 + 2^-8) of the range of V, and fp32's sums
+            err = np.abs(got - o) - (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * 1.1 * np.abs(wl.bf16_bits_to_f64(c.v)).max())
+            assert err.max() <= 0, f"D={D} n={n}"

@@ -436,10 +436,13 @@ FD_API fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void*
  * Scores and sums are taken in fp32. A softmax weight enters the product with V's
  * codes as weight * scale in f16 (11 significant bits), relative to a power of
  * two above the largest V scale (and 2^-64 of the largest V bias) that its warp has
- * seen. V may be of any finite size: no sum on the way is larger than the result. The result of a call is
- * the same bits every time; how a sequence's sum is split over CTAs, and with it
- * the last bits of its result, depends on the other sequences' lengths when
- * num_splits is above 1, but not on the order of the cache's dimensions or pages. */
+ * seen. V may be of any finite size: no sum on the way is larger than the result.
+ * q, K and scale may be of any size whose scores are finite: scale * max|q| *
+ * max|K| * D below 2^126, with the maxima over the G heads of q and the rows of K
+ * that meet. The result of a call is the same bits every time; how a sequence's sum
+ * is split over CTAs, and with it the last bits of its result, depends on the other
+ * sequences' lengths when num_splits is above 1, but not on the order of the cache's
+ * dimensions or pages. */
 FD_API fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4,
                                 const void* v4, const void* params, const int32_t* seqlens,
                                 const int32_t* block_table, float scale, int num_splits,

@@ -382,6 +382,8 @@ struct Int4DecodeArgs {
   bool by_row;            // one cluster per (sequence, KV head), no partial results
   int cluster;            // its CTAs (by_row), at most kInt4MaxCluster
   bool evict_first;       // what is read leaves L2 first
+  float scale_m;          // scale log2(e) = scale_m 2^scale_e, scale_m in [1/2, 1]: the
+  int scale_e;            // product may be beyond fp32 where the scores are not
 };
 
 // D = A B, m16n8k16, f16 inputs, fp32 result.
@@ -775,7 +777,7 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
 // keeps the 8 bits of every bf16 entry down to 2^-24 of the largest.  Then, per
 // token,
 //   t = ks0 S0 + ks1 S1 + (kb0 - 8 ks0) sum_0(q) + (kb1 - 8 ks1) sum_1(q),
-// so that no scale touches an entry.
+// so that no scale touches an entry; the sum starts at minus the reference.
 // P V.  O^T += c^T w on the same MMAs, w = f16(p vs / R) with R a power of
 // two above every |vs| (and 2^-64 of every |vb|) that the warp has seen: f16's 11
 // bits for V of any size.  One more MMA per group sums 8 w as the tensor core sees
@@ -951,6 +953,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
   // 2s, 2s+4 (slots 2 t4, 2 t4 + 1) and 2s+1, 2s+5 (slots 2 t4 + 8, + 9).
   uint32_t qf[NB][2][KW][2][2];
   float sq[NB][2][2], scl[NB][2];      // per column 2 t4 + c: sum of q per group, scale
+  int exps[NB], top_exp = -1024;       // of lane g's heads: the power of two in scl
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     float mx = 0.f;
@@ -967,7 +970,6 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     // mx 2^-e in [1, 2) (rows below 2^-112 stay below 1).
     const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -112), 127);
     const float down = __uint_as_float(static_cast<uint32_t>(141 - e) << 23);    // 2^(14 - e)
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);      // 2^e
     float sum[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -992,18 +994,29 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
     }
     // S holds q 2^(14 - e) (c 2^-24): the sums of q take the same factor, and
     // the scale its inverse, 2^(e + 10).
-    const float sc = a.scale_log2 * up * 1024.f;
+    exps[nb] = e + 10 + p.scale_e;
+    if (mx > 0.f) top_exp = max(top_exp, exps[nb]);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int from = 8 * t4 + 4 * c;                // a lane of head 2 t4 + c
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) sq[nb][h][c] = __shfl_sync(0xffffffffu, sum[h] * 0x1p-24f, from);
-      scl[nb][c] = __shfl_sync(0xffffffffu, sc, from);
-    }
+      for (int h = 0; h < 2; ++h) sq[nb][h][c] = __shfl_sync(0xffffffffu, sum[h] * 0x1p-24f, 8 * t4 + 4 * c);
+  }
+  // Where the largest of the heads' powers is not within 2^+-100 (q next to bf16's ends),
+  // K takes the rest of it.
+  top_exp = __reduce_max_sync(0xffffffffu, top_exp);
+  const int k_exp = top_exp == -1024 ? 0 : min(max(top_exp - min(max(top_exp, -100), 100), -126), 127);
+  const uint32_t k_power = static_cast<uint32_t>(127 + k_exp) * 0x00800080u;     // 2^k_exp, two bf16
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const float sc = p.scale_m * __uint_as_float(static_cast<uint32_t>(127 + min(max(exps[nb] - k_exp, -125), 127)) << 23);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) scl[nb][c] = __shfl_sync(0xffffffffu, sc, 8 * t4 + 4 * c);   // a lane of head 2 t4 + c
   }
 
-  // ---- softmax state.  Per column: the reference (log2 units; a weight is
-  // 2^(t scl - ref)) and the t beyond which it moves.
+  // ---- softmax state.  Per column: the reference, a t whose weight is 2^7, and how far
+  // beyond it t may be before it moves.  t is taken relative to it (a weight is
+  // 2^(t scl + 7)), so that no weight passes 2^15 however large the scores are: the
+  // difference of two rounded numbers of 2^23 and more would.
   float ref[NB][2], bound[NB][2], l_run[NB][2], bias[NB][2][2];
   float acc[NB][2][MB][4], eight[NB][4];              // c w; 8 w of group 0 and of group 1
   float inv_r[2] = {0x1p126f, 0x1p126f};              // 1 / R per group
@@ -1082,10 +1095,11 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       const uint32_t inv_r2 = __byte_perm(__float_as_uint(inv_r[0]), __float_as_uint(inv_r[1]), 0x7632);
 #pragma unroll
       for (int x = 0; x < kUnit / 32; ++x) {
-        const float ks0 = bf16_lo(rec[x].x), ks1 = bf16_lo(rec[x].y);
+        const uint32_t k0 = mul_bf16x2(rec[x].x, k_power), k1 = mul_bf16x2(rec[x].y, k_power);
+        const float ks0 = bf16_lo(k0), ks1 = bf16_lo(k1);
         const int at = 32 * x + lane;
         *reinterpret_cast<float4*>(st + L::kP + at * 16) =
-            make_float4(ks0, fmaf(-8.f, ks0, bf16_hi(rec[x].x)), ks1, fmaf(-8.f, ks1, bf16_hi(rec[x].y)));
+            make_float4(ks0, fmaf(-8.f, ks0, bf16_hi(k0)), ks1, fmaf(-8.f, ks1, bf16_hi(k1)));
         *reinterpret_cast<float2*>(v_recs + at * 8) =
             make_float2(bf16_lo(rec[x].z) * inv_r[0], bf16_lo(rec[x].w) * inv_r[1]);
         *reinterpret_cast<uint32_t*>(v_recs + kUnit * 8 + at * 4) =
@@ -1094,7 +1108,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
       __syncwarp();
     }
 
-    // Scores, t[..][row][column].
+    // Scores less the reference, t[..][row][column].
     float t[NB][BB][2][2], scs[BB][NB][2][4];
 #pragma unroll
     for (int bb = 0; bb < BB; ++bb) {
@@ -1139,7 +1153,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = rec.y * sq[nb][0][c];
+            float x = fmaf(rec.y, sq[nb][0][c], -ref[nb][c]);
             x = fmaf(rec.w, sq[nb][1][c], x);
             x = fmaf(rec.x, sc[nb][0][2 * r + c], x);
             t[nb][bb][r][c] = fmaf(rec.z, sc[nb][1][2 * r + c], x);
@@ -1178,10 +1192,14 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
           for (int off = 4; off < 32; off <<= 1)
             top[nb][c] = fmaxf(top[nb][c], __shfl_xor_sync(0xffffffffu, top[nb][c], off));
           if (top[nb][c] > bound[nb][c]) {
-            const float now = fmaf(top[nb][c], scl[nb][c], -kWeightLog2);
-            const float al = bound[nb][c] == -INFINITY ? 0.f : ex2(ref[nb][c] - now);
-            ref[nb][c] = now;
-            bound[nb][c] = top[nb][c] + fminf(kRescaleLog2 / scl[nb][c], 3e38f);
+            const float al = bound[nb][c] == -INFINITY ? 0.f : ex2(-top[nb][c] * scl[nb][c]);
+            ref[nb][c] += top[nb][c];
+            bound[nb][c] = fminf(kRescaleLog2 / scl[nb][c], 3e38f);
+#pragma unroll
+            for (int bb = 0; bb < BB; ++bb) {
+              t[nb][bb][0][c] -= top[nb][c];
+              t[nb][bb][1][c] -= top[nb][c];
+            }
             if (i == 0) continue;
             l_run[nb][c] *= al;
 #pragma unroll
@@ -1212,7 +1230,7 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
           float e[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], -ref[nb][c]));
+            e[c] = ex2(fmaf(t[nb][bb][r][c], scl[nb][c], kWeightLog2));
             l_run[nb][c] += e[c];
             bias[nb][0][c] = fmaf(e[c], bf16_lo(vb), bias[nb][0][c]);
             bias[nb][1][c] = fmaf(e[c], bf16_hi(vb), bias[nb][1][c]);
@@ -1323,9 +1341,10 @@ __global__ void __launch_bounds__((SH::WARPS + kInt4CopyWarps) * 32, SH::CTAS)
         }
       }
       if (g == 0) {
-        const float lse = (ref[nb][c] + log2f(l_run[nb][c])) * 0.69314718055994530942f;
+        const float at0 = fmaf(ref[nb][c], scl[nb][c], -kWeightLog2);     // the score of weight 1
+        const float lse = (at0 + log2f(l_run[nb][c])) * 0.69314718055994530942f;
         if (state) {
-          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : ref[nb][c];
+          f[L::kM + col] = l_run[nb][c] == 0.f ? -INFINITY : at0;
           f[L::kL + col] = l_run[nb][c];
         } else if (!whole) {
           if (col < a.G) a.part_lse[prow] = lse;

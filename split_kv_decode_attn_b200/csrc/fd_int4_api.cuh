@@ -292,8 +292,7 @@ fd_status fd_decode_int4(const fd_problem* p, const void* q, const void* k4, con
   a.block_size = p->block_size;
   a.log2_block_size = p->block_size ? ilog2(p->block_size) : 0;
   a.max_blocks_per_seq = p->max_blocks_per_seq;
-  a.scale_log2 = scale * 1.4426950408889634074f;
-  a.scale = scale;
+  d.scale_m = static_cast<float>(std::frexp(static_cast<double>(scale) * 1.4426950408889634074f, &d.scale_e));
   d.B = p->B;
   int sms = 0;
   if (device_sms(dev, &sms) != FD_OK) return FD_ERR_CUDA;

@@ -111,3 +111,98 @@ def test_equal_scores_of_any_size_are_merged_alike(size):
             # most 8 / 15 (1 + 2^-8) of the range of V, and fp32's sums
             err = np.abs(got - o) - (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * 1.1 * np.abs(wl.bf16_bits_to_f64(c.v)).max())
             assert err.max() <= 0, f"D={D} n={n}"
+
+
+# ------------------------------------------------------------------- q and scale
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-12, 3e38])
+def test_zero_query_of_any_scale_gives_the_mean(scale):
+    """Lengths that end inside a unit: a token that does not count has weight 0."""
+    lens = [500, 77, 64, 1, 0, 33]
+    for G, D in ((4, 128), (16, 64)):
+        c = Cache(lens, 2 * G, 2, D, 500, seed=1400)
+        c.q[:] = 0
+        c.scale = float(np.float32(scale))
+        c.on_device()
+        ref = c.oracle()
+        for S in (None, 1, 3, 40):
+            check(*decode(c, S), ref, f"scale={scale} G={G} S={S}")
+
+
+@pytest.mark.parametrize("qlog,klog,scale", [
+    (-120, 0, 1e-8),       # scores of about 0
+    (-120, 0, 2.0 ** 118),
+    (-124, 0, 3e37),
+    (-126, 0, 3e38),       # scale log2(e) is beyond fp32
+    (121, -115, None),
+    (125, -127, 0.5),
+    (121, -115, 1e-3),
+    (60, -60, 1e30),
+    (60, 60, 1e-36),
+    (122, 0, 2.0 ** -122)])
+def test_scores_of_ordinary_size_from_any_q_k_and_scale(qlog, klog, scale):
+    lens = [301, 64, 5, 900]
+    for G, Hkv, D in ((8, 1, 128), (16, 2, 64), (2, 8, 64)):
+        c = Cache(lens, G * Hkv, Hkv, D, 900, seed=1500 + G,
+                  k=wl.f64_to_bf16_bits(wl.bf16_bits_to_f64(rows(51, (4, Hkv, 900, D))) * 2.0 ** klog))
+        c.q = wl.f64_to_bf16_bits(wl.bf16_bits_to_f64(c.q) * 2.0 ** qlog)
+        c.scale = c.scale if scale is None else float(np.float32(scale))
+        c.on_device()
+        ref = c.oracle()
+        for S in (None, 1, 2, 30):
+            check(*decode(c, S), ref, f"G={G} S={S}")
+
+
+def test_scores_next_to_the_largest():
+    """Scores of up to 2^125: the row with the largest one is the result.  Heads of
+    ordinary size, of size 0 and of the smallest size beside it keep theirs."""
+    n, G, D = 700, 8, 128
+    c = Cache([n, 130], G, 1, D, n, seed=1600)
+    q = wl.bf16_bits_to_f64(c.q) * np.array([1, 2.0 ** 121, 0, 2.0 ** -120, 2.0 ** 118, 1, -2.0 ** 121, 2])[:, None]
+    c.q = wl.f64_to_bf16_bits(q)
+    c.on_device()
+    o, lse, tol, ltol = c.oracle()
+    far = [1, 4, 6]
+    near = [0, 2, 3, 5, 7]
+    vmax = np.abs(wl.bf16_bits_to_f64(c.v)).max()
+    for S in (None, 1, 2, 30):
+        out, l = decode(c, S)
+        check(out[:, near], l[:, near], [x[:, near] for x in (o, lse, tol, ltol)], f"S={S}")
+        got = wl.bf16_bits_to_f64(out[:, far].view(torch().int16).cpu().numpy().view(np.uint16))
+        # one weight of 1 (the next score is 2^100 away): V's row with the result's 2^-8
+        # and 2^-11, the weight's f16 rounding, of scale * (code - 8), which is at most
+        # 8 / 15 (1 + 2^-8) of the range of V
+        want = o[:, far]
+        err = np.abs(got - want) - (2.0 ** -8 * np.abs(want) + 2.0 ** -11 * 1.1 * vmax)
+        assert err.max() <= 0
+        err = np.abs(l[:, far].cpu().numpy() - lse[:, far]) - ltol[:, far]
+        assert err.max() <= 0
+
+
+@pytest.mark.parametrize("size", [2.0 ** 18, 2.0 ** 21, 2.0 ** 24, 2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores_that_differ_by_little(size, sign):
+    """Scores of one large size whose differences are the steps of fp32 there: equal
+    rows of K, one of them half as large again (or as small) in the middle, so that
+    a reference that is not the largest score would lose every weight."""
+    n, D = 400, 128
+    for at in (0, 70, 399):
+        k = np.ones((1, 1, n, D))
+        k[0, 0, :, 1::2] = -1.0
+        k[0, 0, at] *= 1.5
+        c = Cache([n], 4, 1, D, n, seed=1700, k=wl.f64_to_bf16_bits(k))
+        q = np.tile(np.where(np.arange(D) % 2, -1.0, 1.0), (1, 4, 1)) * np.array([1, 0.5, 1, 2])[:, None]
+        c.q = wl.f64_to_bf16_bits(sign * q * size / D / c.scale)
+        c.on_device()
+        o, lse, tol, ltol = c.oracle()
+        vmax = np.abs(wl.bf16_bits_to_f64(c.v)).max()
+        for S in (1, 2, 5):
+            out, l = decode(c, S)
+            check(out, l, (o, lse, tol, ltol), f"at={at} S={S}")
+            if S > 1:       # parts meet by their lse, as good as fp32 holds it
+                continue
+            got = wl.bf16_bits_to_f64(out.view(torch().int16).cpu().numpy().view(np.uint16))
+            # The row in the middle alone, or the mean of all others: equal weights, whatever
+            # the reference's rounding makes of them.  2^-8 of the result, 2^-11 of V's size.
+            err = np.abs(got - o) - (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * 1.1 * vmax)
+            assert err.max() <= 0, f"at={at}"

@@ -159,11 +159,21 @@ def _ptr(x) -> Optional[int]:
 _raw_stream = _device = None
 
 
+def _forget_stream():
+    global _raw_stream, _device
+    _raw_stream = _device = None
+
+
+# In a forked child torch has to say again whether CUDA may be used.
+os.register_at_fork(after_in_child=_forget_stream)
+
+
 def _stream(stream) -> Optional[int]:
     global _raw_stream, _device
     if stream is None:
         # The raw handle: building torch's Stream object takes 3.2 us, half of a
-        # small call, and the checks of torch.cuda.current_device() are made once.
+        # small call, and the checks of torch.cuda.current_device() are made once
+        # in a process.
         if _raw_stream is None:
             import torch
             torch.cuda.current_device()

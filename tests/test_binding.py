@@ -114,3 +114,31 @@ def test_static_workspace_wrapper_checks_its_tensors():
     assert "Hkv" in call(q, k, v, prob=fd.make_problem(2, 16, 4, 128, 256))
     assert "(B, Hq, D)" in call(q, k, v, prob=fd.make_problem(2, 32, 2, 128, 256))
     assert "CUDA device" in call(q, k, v)
+
+
+def test_a_forked_child_asks_torch_again_whether_cuda_may_be_used(monkeypatch):
+    """The handles of the first call belong to the process that made it: torch refuses
+    CUDA in a forked child by an error that names the reason."""
+    import os
+
+    def refuse():
+        raise RuntimeError("Cannot re-initialize CUDA in forked subprocess")
+    monkeypatch.setattr(fd, "_raw_stream", lambda device: 7)
+    monkeypatch.setattr(fd, "_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", refuse)
+    assert fd._stream(None) == 7
+    read, write = os.pipe()
+    pid = os.fork()
+    if pid == 0:
+        try:
+            told = str(fd._stream(None))
+        except RuntimeError as e:
+            told = str(e)
+        os.write(write, told.encode())
+        os._exit(0)
+    os.close(write)
+    told = os.read(read, 1000).decode()
+    os.close(read)
+    assert os.waitpid(pid, 0)[1] == 0
+    assert "forked" in told
+    assert fd._stream(None) == 7          # the parent's stay

@@ -14,11 +14,12 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfd.so")
-CALLS_PATH = os.path.join(_HERE, "_fdcall.so")
+CALLS_PATH = os.path.join(_HERE, "_fdcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 FD_OK = 0
 FD_ERR_INVALID_ARGUMENT = -1
@@ -133,19 +134,49 @@ def load_library(path: str = LIB_PATH):
 _calls = None
 
 
+class _CtypesCalls:
+    """The calls of csrc/fdcall.c through ctypes."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def append_int4(self, p, n, k, k_stride, v, v_stride, *rest):
+        return self.lib.fd_append_int4(ctypes.byref(p), n, _ptr(k), k_stride, _ptr(v), v_stride,
+                                       *map(_ptr, rest))
+
+    def expand_int4(self, p, *rest):
+        return self.lib.fd_expand_int4(ctypes.byref(p), *map(_ptr, rest))
+
+    def decode_int4(self, p, q, k4, v4, params, seqlens, table, scale, splits, out, lse, workspace,
+                    size, stream):
+        return self.lib.fd_decode_int4(ctypes.byref(p), _ptr(q), _ptr(k4), _ptr(v4), _ptr(params),
+                                       _ptr(seqlens), _ptr(table), scale, splits, _ptr(out),
+                                       _ptr(lse), _ptr(workspace), max(size, 0), stream)
+
+    def alloc_pages(self, *args):
+        return self.lib.fd_alloc_pages(*args[:5], *map(_ptr, args[5:]))
+
+    def release_pages(self, *args):
+        return self.lib.fd_release_pages(*args[:4], *map(_ptr, args[4:]))
+
+
 def _load_calls():
     """The calls whose time on the host counts (csrc/fdcall.c), on the library's
-    functions."""
+    functions; through ctypes where the module was not built."""
     global _calls
     if _calls is None:
         lib = load_library()
         if not os.path.exists(CALLS_PATH):
-            raise ImportError(f"{CALLS_PATH} is missing; build it with __graft_entry__.build()")
-        from . import _fdcall
-        _fdcall.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                       (lib.fd_append_int4, lib.fd_expand_int4, lib.fd_decode_int4,
-                        lib.fd_alloc_pages, lib.fd_release_pages)))
-        _calls = _fdcall
+            _calls = _CtypesCalls(lib)
+            return _calls
+        from importlib import util
+        spec = util.spec_from_file_location(__name__ + "._fdcall", CALLS_PATH)
+        native = util.module_from_spec(spec)
+        spec.loader.exec_module(native)
+        native.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (lib.fd_append_int4, lib.fd_expand_int4, lib.fd_decode_int4,
+                       lib.fd_alloc_pages, lib.fd_release_pages)))
+        _calls = native
     return _calls
 
 

@@ -1,18 +1,21 @@
 """Build libfd.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and
-_fdcall.so (Python's calls of a part of it, csrc/fdcall.c) with gcc."""
+_fdcall (Python's calls of a part of it, csrc/fdcall.c) with the C compiler."""
 from __future__ import annotations
 
 import glob
 import os
+import shlex
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfd.so")
-CALLS = os.path.join(HERE, "_fdcall.so")
+# Named for the interpreter whose ABI it has.
+CALLS = os.path.join(HERE, "_fdcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,16 +47,28 @@ def build_calls(force: bool = False) -> str:
     src, header = os.path.join(CSRC, "fdcall.c"), os.path.join(ROOT, "include", "fd.h")
     if (force or not os.path.exists(CALLS)
             or os.path.getmtime(CALLS) < max(os.path.getmtime(src), os.path.getmtime(header))):
-        subprocess.check_call(["gcc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC",
-                               "-I", os.path.join(ROOT, "include"),
-                               "-I", sysconfig.get_paths()["include"], src, "-o", CALLS])
+        subprocess.check_call(shlex.split(os.environ.get("CC", "gcc")) + [
+                              "-O2", "-Wall", "-Wextra", "-shared", "-fPIC",
+                              "-I", os.path.join(ROOT, "include"),
+                              "-I", sysconfig.get_paths()["include"], src, "-o", CALLS])
     return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/*.cu into split_kv_decode_attn_b200/libfd.so (skipped when
-    the library is newer than every source), and csrc/fdcall.c beside it."""
-    build_calls(force)
+    the library is newer than every source), and csrc/fdcall.c beside it.  The
+    library does not need the latter: where it cannot be built (no Python.h), its
+    calls go through ctypes."""
+    lib = build_library(force, verbose)
+    try:
+        build_calls(force)
+    except (OSError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"{os.path.basename(CALLS)} could not be built ({e}); calls go through "
+                      "ctypes, which takes a few microseconds more each")
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and os.path.exists(LIB):
         newest = max(os.path.getmtime(p) for p in deps())
         if os.path.getmtime(LIB) >= newest:

@@ -314,7 +314,7 @@ FD_API fd_status fd_combine_strided(int R, int B, int Hq, int D, const float* pa
  *   seqlens   [B] int32 or NULL (all max_len)
  *   k8        [B, Hkv, max_len, D] int8 out, 16-byte aligned
  *   k8_scale  [B, Hkv, ceil(max_len / 64)] fp32 out
- * Returns FD_ERR_UNSUPPORTED for a paged, token-major or fp8 cache. */
+ * Returns FD_ERR_UNSUPPORTED for a paged, token-major, fp8 or 4-bit cache. */
 FD_API fd_status fd_quantize_keys(const fd_problem* p, const void* k_cache,
                                   const int32_t* seqlens, int8_t* k8, float* k8_scale,
                                   fd_stream_t stream);
@@ -370,8 +370,10 @@ FD_API fd_status fd_decode_sparse(const fd_problem* p, const void* q, const void
  * and V together: 4.5 bits an entry at D = 128, 5 at D = 64 (bf16: 16).
  * fd_problem describes the cache as for fd_decode, with kv_dtype = FD_KV_INT4;
  * k_scale, v_scale and fp8_mma are ignored. The entry points below return
- * FD_ERR_INVALID_ARGUMENT for another kv_dtype; fd_decode and the other entry
- * points return it for FD_KV_INT4. */
+ * FD_ERR_INVALID_ARGUMENT for another kv_dtype. For FD_KV_INT4 fd_decode,
+ * fd_decode_partial, fd_decode_sparse and fd_decode_static_workspace return it too,
+ * and fd_quantize_keys returns FD_ERR_UNSUPPORTED, as for every cache that is not
+ * bf16. */
 
 /* Quantises new K and V rows and writes them into a 4-bit cache. Per group of
  * a row, with mn and mx its smallest and largest entry:

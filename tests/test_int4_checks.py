@@ -35,6 +35,24 @@ def test_enum_matches_header_and_other_entry_points_refuse_it():
     assert lib.fd_quantize_keys(ctypes.byref(p), K, None, V, R, None) == UNSUP
 
 
+def test_what_the_header_says_other_entry_points_return_for_it():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = " ".join(open(os.path.join(root, "include", "fd.h")).read().replace("\n *", " ").split())
+    said = re.search(r"For FD_KV_INT4 ([^.]*) return it too, and (\w+) returns (\w+)", text)
+    assert said and said.group(2) == "fd_quantize_keys" and said.group(3) == "FD_ERR_UNSUPPORTED"
+    lib, p = fd.load_library(), ctypes.byref(P())
+    got = {"fd_decode": lib.fd_decode(p, Q, K, V, None, None, 0.1, 1, O, None, None, 0, None),
+           "fd_decode_partial": lib.fd_decode_partial(p, Q, K, V, None, None, 0.1, 1, O, W, None, 0,
+                                                      None),
+           "fd_decode_sparse": lib.fd_decode_sparse(p, Q, K, V, W, S, None, 0.1, 1.0, 1, O, None,
+                                                    None, None, 0, None)}
+    for name, status in got.items():     # fd_decode_static_workspace asks the device first
+        assert name in said.group(1) and status == BAD, name
+    assert lib.fd_quantize_keys(p, K, None, V, R, None) == UNSUP
+
+
 def test_decode_int4_refusals():
     assert decode(None) == BAD
     for name in ("q", "k", "v", "r", "out"):

@@ -383,7 +383,9 @@ FD_API fd_status fd_decode_sparse(const fd_problem* p, const void* q, const void
  * before bf16; mn + 8 s is rounded once to fp32, then to bf16). A group whose
  * entries are all equal gets s = 0, c = 8. A group that holds a NaN or an
  * infinity gets s = b = NaN, so that attention over it gives NaN, as it does
- * over a bf16 cache.
+ * over a bf16 cache. s and b are rounded, so that a code may stand for a value
+ * beyond mn .. mx by about 2^-7 of the larger of |mn| and |mx|; next to the largest bf16
+ * that is an infinity once it is rounded to bf16.
  *   p         the cache (max_blocks_per_seq and max_len are checked, not used,
  *             when it is paged; Hq only as Hq % Hkv)
  *   n_tokens  rows of k_new and v_new, >= 0; 0 launches nothing. n_tokens * Hkv

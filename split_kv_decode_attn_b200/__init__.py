@@ -698,7 +698,9 @@ def decode_int4(q, k4, v4, params, seqlens=None, block_table=None, *,
     it).  Paged caches come with block_table [B, max_blocks] int32.  seqlens
     [B] int32 or None.  Returns (out [B, Hq, D] bf16, lse [B, Hq] fp32).
     num_splits (1: one cluster per row; above, the batch is dealt to the SMs) defaults
-    to fd_plan_problem's choice.  Raises ValueError for tensors of the wrong dtype,
+    to fd_plan_problem's choice for sequences of max_len tokens: with a block table of
+    many more places than the sequences hold, pass fd_plan_problem's for their lengths,
+    or 1 for few short ones.  Raises ValueError for tensors of the wrong dtype,
     shape or device, or not contiguous, before anything is launched, and FdError for
     a failing status."""
     import torch

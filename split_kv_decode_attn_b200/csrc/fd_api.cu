@@ -755,9 +755,9 @@ int int4_cluster(int num_sms, long long rows, int longest) {
 // cluster per row, with no second kernel, takes a round of C x 8 x 64 tokens at a time,
 // the longest row the most; dealing takes the mean over the SMs and, for the cut and
 // the merge, about three rounds more, two more than a cluster's merge (64/8 heads, graph
-// replays, clusters against dealt: 1 x 2,048 7.9 and 11.1 us, 1 x 12,288 12.5 and 13.7,
-// 1 x 16,384 14.5 and 14.3, 2 x 8,192 12.7 and 15.6; one CTA per row: 16 x 2,048 14.1
-// and 18.1, 16 x up to 4,096 21.6 and 19.3; a launch of the host is saved too).
+// replays, clusters against dealt: 1 x 2,048 8.0 and 11.4 us, 1 x 12,288 12.8 and 14.0,
+// 1 x 16,384 14.8 and 14.6, 2 x 8,192 13.0 and 15.8; one CTA per row: 16 x 2,048 14.4
+// and 18.3, 16 x up to 4,096 22.1 and 19.6; a launch of the host is saved too).
 int plan_int4(int num_sms, int B, int Hkv, int longest, long long tokens) {
   const long long rows = static_cast<long long>(B) * Hkv, round = 8 * fd::kTile;
   const int c = int4_cluster(num_sms, rows, std::max(longest, 0));

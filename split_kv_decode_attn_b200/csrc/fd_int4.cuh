@@ -668,8 +668,8 @@ __device__ __forceinline__ void int4_copy_warp(const Int4DecodeArgs& p, const CU
 // one at the start of its (drained) rings, and the entries of the result are dealt to
 // the CTAs, which read the states of all.  Two arrivals and a read of the neighbours'
 // shared memory take about 1 us where the partial results in device memory and the
-// second kernel take 4.4 (64/8 heads, D = 128: 1 x 2,048 tokens 7.9 us against 11.1
-// from graph replays; 5 x 3,001, 8/8, D = 64: 9.4 against 12.4).  A unit costs its warp
+// second kernel take 4.4 (64/8 heads, D = 128: 1 x 2,048 tokens 8.0 us against 11.4
+// from graph replays; 5 x 3,001, 8/8, D = 64: 9.4 against 12.5).  A unit costs its warp
 // about 2 us, the same with fewer warps at work, so that a row gains from more CTAs
 // until each warp has one.
 template <int D, class L>

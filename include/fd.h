@@ -440,7 +440,8 @@ FD_API fd_status fd_expand_int4(const fd_problem* p, const void* k4, const void*
  * Scores and sums are taken in fp32. A softmax weight enters the product with V's
  * codes as weight * scale in f16 (11 significant bits), relative to a power of
  * two above the largest V scale (and 2^-64 of the largest V bias) that its warp has
- * seen. V may be of any finite size: no sum on the way is larger than the result.
+ * seen, and counts to 2^-15 of the largest among the 16 tokens beside it; entries of
+ * q count in the same way among 16 channels. V may be of any finite size: no sum on the way is larger than the result.
  * q, K and scale may be of any size whose scores are finite: scale * max|q| *
  * max|K| * D below 2^126, with the maxima over the G heads of q and the rows of K
  * that meet. The result of a call is the same bits every time; how a sequence's sum

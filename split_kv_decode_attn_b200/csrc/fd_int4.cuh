@@ -765,23 +765,28 @@ __device__ __forceinline__ void int4_cluster_merge(const Int4DecodeArgs& p, uint
 // fd_combine_int4_kernel merges them.
 //
 // No code is converted.  A nibble in the low four bits of a half word is the f16
-// subnormal c 2^-24 as it stands, one in the next four bits c 2^-20, both exact
-// on the tensor cores: masks and shifts unpack the codes, 5 operations per 8
+// subnormal c 2^-24 as it stands, one in the next four bits c 2^-20, which the
+// tensor cores multiply as they are: masks and shifts unpack the codes, 5 operations per 8
 // codes of K and 6 of V (whose pairs run along the tokens, so that two tokens'
 // words are merged first).  The e4m3 reading of a nibble, c 2^-9, takes 3, but
 // mma.sync spends 6 conversions on each e4m3 instruction here (measured: 105 a
 // unit, and 38.0 us against 29.7 us at 64K tokens of the CodeLlama-34B heads).
+// What it costs: a subnormal's products are aligned as if it were 2^-14.  Beside a
+// product 8 c w of one MMA another of c w 2^-16 is lost (measured) where c is 2^-24, of
+// c w 2^-20 where it is 2^-20, and of c w 2^-21, fp32's own end, from 2^-18 on.  So a code
+// step counts to 2^-15 of the largest factor of its 16: weights within 2^5 of the
+// largest, and entries of q within 2^8, are taken exactly.  (Codes at 2^-20 alone would
+// take 64 more shifts a unit.)
 // Scores.  S^T = c q^T on m16n8k16 f16 MMAs (16 tokens by up to 8 heads), one
 // fp32 sum per group of channels.  q is scaled by a power of two that brings its
-// largest entry to [2^14, 2^15), for the channels in odd nibbles 2^4 less, which
-// keeps the 8 bits of every bf16 entry down to 2^-24 of the largest.  Then, per
-// token,
+// largest entry to [2^14, 2^15), for the channels in odd nibbles 2^4 less, and
+// enters exactly down to 2^-24 of the largest.  Then, per token,
 //   t = ks0 S0 + ks1 S1 + (kb0 - 8 ks0) sum_0(q) + (kb1 - 8 ks1) sum_1(q),
 // so that no scale touches an entry; the sum starts at minus the reference.
 // P V.  O^T += c^T w on the same MMAs, w = f16(p vs / R) with R a power of
 // two above every |vs| (and 2^-64 of every |vb|) that the warp has seen: f16's 11
 // bits for V of any size.  One more MMA per group sums 8 w as the tensor core sees
-// it, which the end takes off: c - 8, with no rounding of w left in it.  The
+// it, which the end takes off: c - 8, with no rounding of w to f16 left in it.  The
 // biases' part sum_j p_j vb_j / R is summed in fp32 beside it; the factor R comes
 // in once the row's sum is divided by that of the weights, so that nothing on the
 // way is larger than the result.  (1 x 65,536 tokens at 64/8 heads 25.3 us, 25.0

@@ -206,3 +206,25 @@ def test_large_scores_that_differ_by_little(size, sign):
             # the reference's rounding makes of them.  2^-8 of the result, 2^-11 of V's size.
             err = np.abs(got - o) - (2.0 ** -8 * np.abs(o) + 2.0 ** -11 * 1.1 * vmax)
             assert err.max() <= 0, f"at={at}"
+
+
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 30, 2.0 ** 60, 2.0 ** 120])
+def test_equal_scores_over_many_units_of_a_warp(size):
+    """The same score over and over, in units that each take it relative to a reference
+    from an earlier one: finite, within V's range, and within the bound of the oracle."""
+    n, D = 9000, 128
+    k = np.ones((1, 1, n, D))
+    k[..., 1::2] = -1.0
+    c = Cache([n], 8, 1, D, n, seed=1800, k=wl.f64_to_bf16_bits(k))
+    q = np.tile(np.where(np.arange(D) % 2, -1.0, 1.0), (1, 8, 1)) * np.linspace(0.1, 1, 8)[:, None]
+    c.q = wl.f64_to_bf16_bits(q * size / D / c.scale)
+    c.on_device()
+    ref = c.oracle()
+    v = wl.bf16_bits_to_f64(c.v)[0, 0]
+    for S in (1, 2, 11):
+        out, lse = decode(c, S)
+        check(out, lse, ref, f"S={S}")
+        got = wl.bf16_bits_to_f64(out.view(torch().int16).cpu().numpy().view(np.uint16))
+        # the values of the codes pass V by 2^-7 of its size, the result by 2^-8
+        room = 2.0 ** -6 * np.abs(v).max()
+        assert (got <= v.max(0) + room).all() and (got >= v.min(0) - room).all()
